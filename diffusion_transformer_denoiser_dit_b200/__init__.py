@@ -4,6 +4,6 @@ Everything the forward computes runs in libdit_b200.so; this package only marsha
 arguments (see binding.py).  Build the library with
 ``python -m diffusion_transformer_denoiser_dit_b200.build``.
 """
-from .binding import DiT, DitError, linear_bf16, load  # noqa: F401
+from .binding import DiT, DitError, Rotary, attention_packed, linear_bf16, linear_fused, load  # noqa: F401
 
-__all__ = ["DiT", "DitError", "linear_bf16", "load"]
+__all__ = ["DiT", "DitError", "Rotary", "attention_packed", "linear_bf16", "linear_fused", "load"]

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int, c_uint16, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int, c_longlong, c_uint16, c_void_p
 from typing import Optional, Sequence
 
 import numpy as np
@@ -20,6 +20,10 @@ DIT_ERR_DEVICE_TIMEOUT, DIT_ERR_BAD_LABEL, DIT_ERR_NO_DEVICE = 5, 6, 7
 DIT_OPT_FORCE_GUIDANCE, DIT_OPT_USE_GRAPH, DIT_OPT_OVERLAP_LAUNCH, DIT_OPT_CFG_CHANNELS = 1, 2, 3, 4
 DIT_OPT_REPEAT_KIND, DIT_OPT_SPLIT_K, DIT_OPT_PAIR_GEMM = 5, 6, 7
 DIT_SAMPLER_DDIM, DIT_SAMPLER_EULER = 0, 1
+DIT_DTYPE_F32, DIT_DTYPE_BF16, DIT_DTYPE_FP16 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu_tanh": 2, "gelu": 3, "silu": 4}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROTARY_MAX_PAIRS = 256
 
 # every exported symbol declared in include/dit.h
 EXPORTS = [
@@ -27,7 +31,8 @@ EXPORTS = [
     "dit_status_string", "dit_destroy", "dit_set_option", "dit_debug_residual", "dit_debug_condition",
     "dit_debug_wait_probe", "dit_op_linear_bf16", "dit_forward_launch_count", "dit_profile_enable",
     "dit_profile_read", "dit_condition_static", "dit_op_linear_bf16_pair", "dit_sampler_step", "dit_sample",
-    "dit_op_attention_bf16", "dit_debug_attention_rescales", "dit_op_linear_e4m3",
+    "dit_op_attention_bf16", "dit_debug_attention_rescales", "dit_op_linear_e4m3", "dit_op_linear_fused",
+    "dit_op_attention_packed", "dit_rotary_frequencies", "dit_rotary_init", "dit_op_rotary",
 ]
 
 KERNEL_KINDS = ["cond", "adaln", "patch", "ln", "qkv", "attn", "proj", "fc1", "fc2", "decode", "sampler"]
@@ -40,6 +45,12 @@ class DitConfig(ctypes.Structure):
                 ("qk_norm", c_int), ("cond_kind", c_int), ("num_classes", c_int), ("freq_dim", c_int),
                 ("max_batch", c_int), ("t_scale", c_float), ("block_kind", c_int), ("ffn_fp8", c_int),
                 ("attn_fp8", c_int)]
+
+
+class RotaryPlan(ctypes.Structure):
+    """dit_rotary of include/dit.h."""
+    _fields_ = [("pairs", c_int), ("axes", c_int), ("amplitude", c_float),
+                ("turns", ctypes.c_uint64 * ROTARY_MAX_PAIRS)]
 
 
 class DitError(RuntimeError):
@@ -59,7 +70,7 @@ def load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is missing: build it with python -m diffusion_transformer_denoiser_dit_b200.build")
     lib = ctypes.CDLL(LIB_PATH)
-    P = c_void_p
+    P, L = c_void_p, c_longlong
     sig = {
         "dit_create": (c_int, [POINTER(DitConfig), POINTER(c_void_p), c_int, POINTER(c_void_p)]),
         "dit_weight_count": (c_int, [POINTER(DitConfig)]),
@@ -85,6 +96,12 @@ def load() -> ctypes.CDLL:
         "dit_op_attention_bf16": (c_int, [P, P, P, P, c_int, c_int, c_int, c_int, P, P]),
         "dit_debug_attention_rescales": (c_int, [P, POINTER(ctypes.c_longlong)]),
         "dit_op_linear_e4m3": (c_int, [P, P, P, P, P, P, c_int, c_int, c_int, c_int, P]),
+        "dit_op_linear_fused": (c_int, [c_int, P, L, P, L, P, c_int, P, L, P, L, c_int, c_int, c_int, c_int, P, P]),
+        "dit_op_attention_packed": (c_int, [c_int] + [P] * 7 + [c_int] * 8 + [POINTER(L), c_float, c_int, P, P]),
+        "dit_rotary_frequencies": (c_int, [c_int, c_int, c_double, c_double, c_int, POINTER(c_double),
+                                           POINTER(c_float)]),
+        "dit_rotary_init": (c_int, [POINTER(RotaryPlan), POINTER(c_double), c_int, c_int, c_float]),
+        "dit_op_rotary": (c_int, [POINTER(RotaryPlan), c_int, P, L, L, P, c_int, P, L, L] + [c_int] * 5 + [P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -301,3 +318,203 @@ def linear_e4m3(x8, w8, sx, sw, b, block_n: int = 128, stream=None):
     if rc != DIT_OK:
         raise DitError(rc, f"dit_op_linear_e4m3: {status_string(rc)}")
     return y
+
+
+# ---------------------------------------------------------------- building blocks of packed layers
+
+
+def _codes():
+    import torch
+    return {torch.float32: DIT_DTYPE_F32, torch.bfloat16: DIT_DTYPE_BF16, torch.float16: DIT_DTYPE_FP16}
+
+
+_DTYPE_CODES = None
+
+
+def _dtype_code(dtype, floats32: bool, what: str) -> int:
+    global _DTYPE_CODES
+    if _DTYPE_CODES is None:
+        _DTYPE_CODES = _codes()
+    code = _DTYPE_CODES.get(dtype, -1)
+    if code < 0 or (code == DIT_DTYPE_F32 and not floats32):
+        raise TypeError(f"{what}: dtype {dtype} is not supported")
+    return code
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _call(fn, name: str, tensors, stream, *args):
+    """fn(*args, stream) on the tensors' device and stream; raises DitError on a refusal."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: tensors on {t.device} and {dev}")
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: needs CUDA tensors")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, name, tensors, stream, *args)
+    current = torch.cuda.current_stream()
+    if stream is None:
+        stream = current
+    elif stream != current:
+        if stream.device != dev:
+            raise ValueError(f"{name}: stream on {stream.device}, tensors on {dev}")
+        for t in tensors:  # their memory is not given away before the work on this stream is done
+            if t is not None:
+                t.record_stream(stream)
+    rc = fn(*args, stream.cuda_stream)
+    if rc != DIT_OK:
+        raise DitError(rc, f"{name}: {status_string(rc)}")
+
+
+def _fresh(shape, dtype, device, stream):
+    """An output on the stream that will write it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def linear_fused(x, w, bias=None, act: str = "none", residual=None, out=None, out_dtype=None, status=None, stream=None):
+    """out = act(x w^T + bias) + residual (dit_op_linear_fused in include/dit.h).
+
+    x [M, K] and w [N, K]: bf16 or fp16 CUDA tensors, last stride 1; bias float32 [N]; act one of
+    ACTIVATIONS; residual [M, N] of out's dtype (a stride-0 row broadcasts); out [M, N] of x's
+    dtype or float32, residual itself for an update in place; status int32 [1] (zeroed) receives
+    a timeout.  Returns out."""
+    lib = load()
+    _need(x.dim() == 2 and w.dim() == 2 and x.shape[1] == w.shape[1], "linear_fused: x [M, K] and w [N, K]")
+    (M, K), N = x.shape, w.shape[0]
+    code = _dtype_code(x.dtype, False, "linear_fused")
+    _need(w.dtype == x.dtype, "linear_fused: x and w of one dtype")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"linear_fused: act {act!r} is none of {sorted(ACTIVATIONS)}")
+    if out is None:
+        out = _fresh((M, N), x.dtype if out_dtype is None else out_dtype, x.device, stream)
+    _need(tuple(out.shape) == (M, N) and (out_dtype is None or out.dtype == out_dtype),
+          "linear_fused: out [M, N] of out_dtype")
+    ocode = _dtype_code(out.dtype, True, "linear_fused")
+    _need(_last1(x) and _last1(w) and _last1(out), "linear_fused: last strides must be 1")
+    if bias is not None:
+        _need(bias.shape == (N,) and _DTYPE_CODES.get(bias.dtype) == DIT_DTYPE_F32 and _last1(bias),
+              "linear_fused: bias float32 [N]")
+    ldr = 0
+    if residual is not None:
+        _need(residual.shape == out.shape and residual.dtype == out.dtype and _last1(residual),
+              "linear_fused: residual [M, N] of out's dtype")
+        ldr = residual.stride(0)
+    _call(lib.dit_op_linear_fused, "linear_fused", (x, w, out, bias, residual, status), stream, code, x.data_ptr(),
+          x.stride(0) if M > 1 else 0, w.data_ptr(), w.stride(0) if N > 1 else 0, _ptr(bias), ACTIVATIONS[act],
+          _ptr(residual), ldr, out.data_ptr(), out.stride(0) if M > 1 else N, ocode, M, N, K, _ptr(status))
+    return out
+
+
+def _last1(t) -> bool:
+    return t.stride(-1) == 1 or t.shape[-1] == 1
+
+
+def _strides(t):
+    """Token and head stride of [tokens, heads, features]; those of a length-1 axis are free."""
+    n, h, d = t.shape
+    sh = t.stride(1) if h > 1 else -(-d // 8) * 8
+    return (t.stride(0) if n > 1 else h * sh), sh
+
+
+def attention_packed(q, k, v, cu_q, cu_k, max_q: int, max_k: int, causal: bool = False, scale=None, out=None,
+                     return_lse: bool = False, status=None, stream=None):
+    """Attention over packed sequences (dit_op_attention_packed in include/dit.h).
+
+    q [total_q, heads, dh], k and v [total_k, kv_heads, dh]: bf16 or fp16 CUDA tensors, last
+    stride 1; cu_q, cu_k int32 CUDA [n + 1]: the sequences' offsets; max_q, max_k: the longest
+    lengths; causal aligns the last query with the last key; scale defaults to dh^-0.5.
+    Returns out (rows outside every sequence are not written; a new out starts undefined
+    there), or (out, lse float32 [heads, total_q]) with return_lse."""
+    lib = load()
+    _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3 and k.shape == v.shape and q.shape[2] == k.shape[2],
+          "attention_packed: q [total_q, heads, dh], k and v [total_k, kv_heads, dh]")
+    (tq, h, d), (tk, hk, _) = q.shape, k.shape
+    code = _dtype_code(q.dtype, False, "attention_packed")
+    _need(k.dtype == q.dtype and v.dtype == q.dtype, "attention_packed: q, k and v of one dtype")
+    if out is None:
+        out = _fresh((tq, h, d), q.dtype, q.device, stream)
+    _need(out.shape == q.shape and out.dtype == q.dtype, "attention_packed: out like q")
+    _need(_last1(q) and _last1(k) and _last1(v) and _last1(out), "attention_packed: last strides must be 1")
+    n = cu_q.shape[0] - 1
+    _need(cu_q.dim() == 1 and n >= 0 and cu_k.shape == cu_q.shape and cu_q.is_contiguous() and cu_k.is_contiguous()
+          and not (cu_q.dtype.is_floating_point or cu_k.dtype.is_floating_point) and cu_q.element_size() == 4
+          and cu_k.element_size() == 4, "attention_packed: cu_q and cu_k contiguous int32 [n + 1]")
+    lse = _fresh((h, tq), _f32(), q.device, stream) if return_lse else None
+    strides = (c_longlong * 8)(*_strides(q), *_strides(k), *_strides(v), *_strides(out))
+    _call(lib.dit_op_attention_packed, "attention_packed", (q, k, v, out, lse, cu_q, cu_k, status), stream, code,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), cu_q.data_ptr(), cu_k.data_ptr(), n, tq,
+          tk, int(max_q), int(max_k), h, hk, d, strides, float(d ** -0.5 if scale is None else scale), int(causal),
+          _ptr(status))
+    return (out, lse) if return_lse else out
+
+
+def _f32():
+    import torch
+    return torch.float32
+
+
+class Rotary:
+    """Rotary positions for heads of head_dim features, of which the first rotary_dim turn
+    (dit_op_rotary in include/dit.h).  axes coordinates per token split the turned features
+    evenly; scaling is one of ROTARY_SCALINGS with its factor (and original_length for "yarn");
+    freqs (radians per position, one per pair of an axis) replaces base and scaling."""
+
+    def __init__(self, head_dim: int, rotary_dim: Optional[int] = None, interleaved: bool = False,
+                 base: float = 10000.0, axes: int = 1, scaling: str = "none", factor: float = 1.0,
+                 original_length: int = 0, freqs: Optional[Sequence[float]] = None):
+        self.lib = load()
+        self.head_dim, self.axes, self.interleaved = int(head_dim), int(axes), bool(interleaved)
+        part = self.head_dim if rotary_dim is None else int(rotary_dim)
+        _need(self.axes > 0 and 0 < part <= self.head_dim and part % (2 * self.axes) == 0,
+              "Rotary: rotary_dim must be a multiple of 2 * axes and at most head_dim")
+        each = part // (2 * self.axes)
+        if scaling not in ROTARY_SCALINGS:
+            raise ValueError(f"Rotary: scaling {scaling!r} is none of {sorted(ROTARY_SCALINGS)}")
+        f, amp = (c_double * each)(), c_float(1.0)
+        if freqs is not None:
+            _need(len(freqs) == each, f"Rotary: freqs needs {each} entries")
+            f[:] = [float(v) for v in freqs]
+        else:
+            self._check(self.lib.dit_rotary_frequencies(ROTARY_SCALINGS[scaling], each, float(base), float(factor),
+                                                        int(original_length), f, ctypes.byref(amp)),
+                        "dit_rotary_frequencies")
+        self._plan = RotaryPlan()
+        self._check(self.lib.dit_rotary_init(ctypes.byref(self._plan), f, each, self.axes, amp), "dit_rotary_init")
+        self._ref = ctypes.byref(self._plan)
+
+    @staticmethod
+    def _check(rc: int, what: str):
+        if rc != DIT_OK:
+            raise DitError(rc, f"{what}: {status_string(rc)}")
+
+    def apply(self, x, positions, out=None, transpose: bool = False, stream=None):
+        """x [tokens, heads, head_dim] (float32, bf16 or fp16) turned by positions [tokens] or
+        [tokens, axes] (int32 or int64); out=x turns in place.  transpose: the gradient of x
+        from that of the result."""
+        _need(x.dim() == 3 and x.shape[2] == self.head_dim, "Rotary.apply: x [tokens, heads, head_dim]")
+        code = _dtype_code(x.dtype, True, "Rotary.apply")
+        if out is None:
+            out = _fresh(tuple(x.shape), x.dtype, x.device, stream)
+        _need(out.shape == x.shape and out.dtype == x.dtype and _last1(x) and _last1(out),
+              "Rotary.apply: out like x, last strides 1")
+        n = x.shape[0]
+        _need(positions.is_contiguous() and not positions.dtype.is_floating_point
+              and positions.element_size() in (4, 8)
+              and (positions.shape == (n, self.axes) or (self.axes == 1 and positions.shape == (n,))),
+              "Rotary.apply: positions contiguous int32 or int64 [tokens, axes]")
+        xt, xh = _strides(x)
+        yt, yh = _strides(out)
+        _call(self.lib.dit_op_rotary, "Rotary.apply", (x, positions, out), stream, self._ref, code, x.data_ptr(), xt, xh,
+              positions.data_ptr(), int(positions.element_size() == 8), out.data_ptr(), yt, yh, n, x.shape[1],
+              self.head_dim, int(self.interleaved), int(transpose))
+        return out

@@ -58,7 +58,7 @@ typedef enum {
   DIT_ERR_NO_DEVICE = 7       /* no sm_100 device is current */
 } dit_status;
 
-enum { DIT_DTYPE_F32 = 0, DIT_DTYPE_BF16 = 1 };
+enum { DIT_DTYPE_F32 = 0, DIT_DTYPE_BF16 = 1, DIT_DTYPE_FP16 = 2 }; /* FP16: dit_op_* of packed layers only */
 enum { DIT_POS_SINCOS2D = 0, DIT_POS_ROPE3D = 1 };
 enum { DIT_COND_CLASS = 0, DIT_COND_VECTOR = 1 };
 /* How the condition enters the blocks: the four designs "확산 트랜스포머" (itwiki.kr) compares
@@ -392,6 +392,106 @@ dit_status dit_debug_attention_rescales(dit_handle* h, long long* count);
 /* Number of kernel launches one dit_forward enqueues for batch B (graph nodes if a
    graph is replayed). */
 int dit_forward_launch_count(const dit_handle* h, int B, float cfg_scale);
+
+/* ------------------------------------------------------------------------------ */
+/* Building blocks of a layer over packed sequences (latents of different sizes in  */
+/* one batch, prompts of a text encoder).  dtype is DIT_DTYPE_BF16 or              */
+/* DIT_DTYPE_FP16 (16-bit patterns); strides are in elements.  No block allocates,  */
+/* keeps anything between calls or synchronises, so any number may be in flight on  */
+/* any streams and in captured graphs.  status: dev int32 or NULL; it receives      */
+/* DIT_ERR_DEVICE_TIMEOUT if a bounded wait in the kernel runs out (0 stays 0).     */
+/* ------------------------------------------------------------------------------ */
+
+enum { DIT_ACT_NONE = 0, DIT_ACT_RELU = 1, DIT_ACT_GELU_TANH = 2, DIT_ACT_GELU = 3, DIT_ACT_SILU = 4 };
+
+/*
+ * dit_op_linear_fused — matrix product with its epilogue:
+ *   y[m, n] = act(sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n]
+ * x [M, K] rows ldx apart, w [N, K] rows ldw apart: dev, dtype; bias: dev float32 [N] or NULL;
+ * act: DIT_ACT_* (GELU_TANH is the tanh form, GELU the erf form); residual [M, N] rows ldr
+ * apart, of y's type, or NULL; y [M, N] rows ldy apart: out_dtype = dtype or DIT_DTYPE_F32.
+ * y may be residual itself (same ldr and ldy: an update in place) and must not overlap
+ * anything else.  Sums and epilogue are float32, rounded once at the end; with a float32 y
+ * the tensor cores' running sum is moved to registers every 512 products, so that its
+ * truncation does not add up over K.  Any M >= 0, N, K >= 1, strides and element alignment;
+ * rows of x and w that start on 16-byte boundaries are read by TMA, others by plain loads.
+ * DIT_ERR_INVALID_ARG: null pointers, negative sizes or strides, ldy < N, an unknown act.
+ * DIT_ERR_UNSUPPORTED: another dtype or out_dtype.
+ */
+dit_status dit_op_linear_fused(int dtype, const void* x, long long ldx, const void* w, long long ldw, const float* bias,
+                               int act, const void* residual, long long ldr, void* y, long long ldy, int out_dtype,
+                               int M, int N, int K, int* status, dit_stream_t stream);
+
+/*
+ * dit_op_attention_packed — attention over sequences of different lengths, packed without
+ * padding.  Sequence s owns the query tokens cu_q[s] .. cu_q[s+1]-1 and the key tokens
+ * cu_k[s] .. cu_k[s+1]-1; for its query i (of nq) and head h,
+ *   o_i = sum_j p_ij v_j,  p_ij = softmax_j(scale q_i . k_j),  j over the nk keys of s, or
+ *   with causal over j <= i + nk - nq (the last query sees every key),
+ * k and v of head h / (heads / kv_heads).  A query that sees no key gets o = 0, lse = -inf.
+ * q, o [total_q, heads, dh]; k, v [total_k, kv_heads, dh]: dev, dtype, features contiguous,
+ * 16-byte aligned; strides: host long long[8] = token and head strides of q, k, v, o in
+ * elements, multiples of 8.  lse: dev float32 [heads, total_q] (log of the sum of
+ * exp(scale q.k)) or NULL.  cu_q, cu_k: dev int32 [n_seq + 1], non-decreasing, cu_q[n_seq] <=
+ * total_q, cu_k[n_seq] <= total_k; query rows outside every sequence are left as they were, key
+ * rows outside are not used.  Offsets beyond the totals are cut to them.  max_q, max_k: the
+ * longest query and key length, which only choose how the work is split.
+ * nq = 1 is the form for single new tokens over a cache.  The scores stay float32; the
+ * probabilities are rounded to dtype for the product with v, their sum is not.  v's rows
+ * within a sequence have to be finite (a masked probability is 0, and 0 * inf is NaN).
+ * DIT_ERR_UNSUPPORTED: another dtype, dh not a multiple of 8 or above 128, more than 128
+ * heads per key head.  DIT_ERR_INVALID_ARG: null pointers, negative sizes, heads not a
+ * multiple of kv_heads, misaligned pointers or strides, o rows that overlap, scale <= 0.
+ */
+dit_status dit_op_attention_packed(int dtype, const void* q, const void* k, const void* v, void* o, float* lse,
+                                   const int* cu_q, const int* cu_k, int n_seq, int total_q, int total_k, int max_q,
+                                   int max_k, int heads, int kv_heads, int dh, const long long* strides, float scale,
+                                   int causal, int* status, dit_stream_t stream);
+
+/* Scalings of rotary frequencies f_i = base^(-i / pairs) for positions beyond those that a
+   model was trained on (factor s):
+   LINEAR  f_i / s (interpolated positions);
+   NTK     base multiplied by s^(pairs / (pairs - 1)): the slowest pair is interpolated, the
+           fastest keeps its frequency;
+   YARN    g f_i + (1 - g) f_i / s with g = clamp((original_length f_i / 2 pi - 1) / 31, 0, 1),
+           and cos, sin times 0.1 ln s + 1 (s > 1). */
+enum { DIT_ROTARY_NONE = 0, DIT_ROTARY_LINEAR = 1, DIT_ROTARY_NTK = 2, DIT_ROTARY_YARN = 3 };
+enum { DIT_ROTARY_MAX_PAIRS = 256 };
+
+/* A rotation, a plain host value that owns nothing; filled by dit_rotary_init. */
+typedef struct dit_rotary {
+  int pairs, axes;                      /* all pairs of a head; position coordinates per token */
+  float amplitude;                      /* multiplies cos and sin */
+  uint64_t turns[DIT_ROTARY_MAX_PAIRS]; /* of the pairs of one axis: turns per position * 2^64 */
+} dit_rotary;
+
+/* The frequencies (radians per position) of the `pairs` pairs of one axis into freq (host
+   double[pairs]) and the amplitude.  original_length is read by YARN only.
+   DIT_ERR_INVALID_ARG: null pointers, pairs < 1 (< 2 for NTK), base or factor not positive and
+   finite, an unknown scaling, original_length < 1 for YARN. */
+dit_status dit_rotary_frequencies(int scaling, int pairs, double base, double factor, int original_length, double* freq,
+                                  float* amplitude);
+
+/* Fill r from any frequencies (host double[pairs_per_axis]).  With `axes` coordinates per
+   token, axis a turns the pairs a * pairs_per_axis .. (a + 1) * pairs_per_axis - 1.
+   DIT_ERR_UNSUPPORTED: more than DIT_ROTARY_MAX_PAIRS pairs in all. */
+dit_status dit_rotary_init(dit_rotary* r, const double* freq, int pairs_per_axis, int axes, float amplitude);
+
+/*
+ * dit_op_rotary — turn the first 2 * pairs features of every head by its token's position:
+ *   y_a = amp (x_a cos t - x_b sin t),  y_b = amp (x_b cos t + x_a sin t),  t = position * freq_k,
+ * (a, b) = (k, k + pairs), or (2k, 2k + 1) when interleaved; the features behind are copied.
+ * transpose != 0 turns the other way (same amplitude): the gradient of x from that of y.
+ * x, y [tokens, heads, dh]: dev, dtype DIT_DTYPE_F32, BF16 or FP16, token and head strides in
+ * elements; y may be x itself with the same strides, and must not overlap it otherwise.
+ * positions: dev int32 or int64 [tokens, axes], any values.  The angle is reduced to a turn in
+ * 64-bit integers, so far positions lose nothing; the rest is float32, rounded once.
+ * DIT_ERR_INVALID_ARG: null pointers, an r that was not filled, negative sizes or strides, 2 * pairs > dh,
+ * y rows that overlap.  DIT_ERR_UNSUPPORTED: another dtype, heads * dh > 2^24.
+ */
+dit_status dit_op_rotary(const dit_rotary* r, int dtype, const void* x, long long x_tok, long long x_head,
+                         const void* positions, int positions_64bit, void* y, long long y_tok, long long y_head,
+                         int tokens, int heads, int dh, int interleaved, int transpose, dit_stream_t stream);
 
 #ifdef __cplusplus
 }
