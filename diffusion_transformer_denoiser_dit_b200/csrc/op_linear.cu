@@ -75,7 +75,8 @@ static cudaError_t launch_rows(const LinearArgs& a, cudaStream_t st) {
   return run(linear_rows_kernel<T, 8, VEC>, 8);
 }
 
-cudaError_t launch_linear_fused(const LinearArgs& a, int, cudaStream_t st) {
+cudaError_t launch_linear_fused(const LinearArgs& a, int num_sms, cudaStream_t st) {
+  if (a.M > 8) return launch_linear_tc(a, num_sms, st);
   const bool vec = ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w)) & 15) == 0 &&
                    ((a.ldx | a.ldw) & 7) == 0;
   if (a.fp16) return vec ? launch_rows<__half, true>(a, st) : launch_rows<__half, false>(a, st);

@@ -1,0 +1,777 @@
+// y = act(x W^T + b) + r on the tensor cores: two kernels.
+//
+// linear_pair_kernel: 256 x BN output tiles on SM pairs (tcgen05 cta_group::2), persistent.
+//   A pair moves 256 + BN operand rows per 256 x BN x 64 multiply-adds, half of what two single
+//   SMs would.  Warp 0 of each CTA loads its 128 rows of x and BN/2 rows of W per 64-wide K
+//   stage by TMA; one thread of the leader issues the MMAs of both SMs; warps 2-9 of each CTA
+//   finish 32 rows x BN/2 columns each.  Two accumulators in TMEM: the epilogue of one tile
+//   runs beside the main loop of the next.  The residual is loaded by TMA into the staging
+//   tile while the main loop still runs, added there, and stored from there by TMA.
+//
+// linear_split_kernel: 128 x BN tiles, one CTA per tile and K slice; the CTAs of a cluster hold
+//   the slices of one tile, leave their float32 partial tiles in shared memory, and each adds up
+//   and finishes its share of the tile from all of them over distributed shared memory, in the
+//   order of the slices, so that results repeat bit for bit.  For products with too few 256-row
+//   tiles to fill the GPU.  Operands whose rows do not start on 16-byte boundaries are copied
+//   into shared memory by the epilogue warps instead of TMA (GATHER).
+//
+// float32 outputs: tcgen05 drops bits below the accumulator's last place at every 16-wide step,
+// a one-sided error that grows with K (5e-6 of the result's norm at K = 4608, where float32
+// summation has 7e-7).  So the sum is taken over in registers every 512 products, in
+// round-to-nearest.  16-bit outputs (rounded at 2^-9 or 2^-12) run all of K in one go.
+//
+// Every wait is bounded; no TMA multicast.
+#include <type_traits>
+
+#include "internal.h"
+#include "op_common.cuh"
+#include "op_linear.cuh"
+#include "ops.h"
+
+namespace dit {
+
+constexpr int kF32ChunkBlocks = 8;  // 64-wide K blocks per accumulator when the output is float32
+
+// Instruction descriptor, kind::f16: A and B both fp16 or both bf16, K-major, f32 accumulator.
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N) {
+  constexpr uint32_t f = std::is_same<T, __half>::value ? 0u : 1u;
+  return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// v[i] += bias[n + i] for i < W; columns at or past N get nothing
+template <int W>
+__device__ __forceinline__ void add_bias(const LinearArgs& a, int n, float* v) {
+  if (a.bias == nullptr) return;
+  if (n + W <= a.N && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + n + i));
+      v[i] += b.x;
+      v[i + 1] += b.y;
+      v[i + 2] += b.z;
+      v[i + 3] += b.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (n + i < a.N) v[i] += __ldg(a.bias + n + i);
+  }
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// ------------------------------------------------------------------------- SM pairs
+template <int BN, bool F32>
+struct PairCfg {
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, STAGE = A_BYTES + B_BYTES;
+  static constexpr int COLS = BN / 2;             // columns per epilogue warp
+  static constexpr int CW = F32 ? 32 : 64;        // columns per 128-byte staging row
+  static constexpr int CHUNKS = COLS / CW;
+  static constexpr int BUF = 32 * 128;            // one staging tile: 32 rows of 128 bytes
+  static constexpr int STAGING = 8 * 2 * BUF;
+  static constexpr int FIT = (232448 - 1024 - 512 - STAGING) / STAGE;
+  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + STAGING + 512;
+  static_assert(STAGES >= 4 && B_BYTES % 1024 == 0 && CHUNKS >= 1, "tile shape");
+};
+
+template <int BN, typename T, bool F32>
+__global__ void __launch_bounds__(320, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmY,
+                       const LinearArgs a, const int tma_out) {
+  using C = PairCfg<BN, F32>;
+  using O = typename std::conditional<F32, float, T>::type;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t staging = sbase + C::STAGES * C::STAGE;
+  const uint32_t bar0 = staging + C::STAGING;
+  // barriers: stage full, stage empty, accumulator full, accumulator empty, residual landed
+  auto FULL = [&](int s) { return bar0 + 8u * s; };
+  auto EMPTY = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+  auto TFULL = [&](int i) { return bar0 + 8u * (2 * C::STAGES + i); };
+  auto TEMPTY = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 2 + i); };
+  auto RES = [&](int w, int b) { return bar0 + 8u * (2 * C::STAGES + 4 + 2 * w + b); };
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::STAGES * C::STAGE + C::STAGING + 8 * (2 * C::STAGES + 20));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool leader = rank == 0;
+  const int cid = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const int m_tiles = (a.M + 255) / 256, n_tiles = (a.N + BN - 1) / BN, num_tiles = m_tiles * n_tiles;
+  const int kblocks = (a.K + 63) / 64;
+  const int chunk = F32 ? kF32ChunkBlocks : kblocks;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(FULL(s), 1);
+      mbar_init(EMPTY(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(TFULL(i), 1);
+      mbar_init(TEMPTY(i), 512);  // 256 epilogue threads in each CTA of the pair
+    }
+    for (int i = 0; i < 16; ++i) mbar_init(RES(i >> 1, i & 1), 1);
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(holder), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *holder;
+  pdl_trigger();
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {  // ---------------- loads (both CTAs)
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = cid; tile < num_tiles && ok; tile += nclusters) {
+        const int m0 = (tile % m_tiles) * 256 + 128 * rank, n0 = (tile / m_tiles) * BN + BN / 2 * rank;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(EMPTY(s), ph ^ 1u, a.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = sbase + s * C::STAGE, full = mapa_shared(FULL(s), 0);
+          if (leader) mbar_arrive_expect_tx(FULL(s), 2 * C::STAGE);
+          tma_load_2d_pair(sa, &tmX, full, kb * 64, m0);
+          tma_load_2d_pair(sa + C::A_BYTES, &tmW, full, kb * 64, n0);
+          if (++s == C::STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // every stage this CTA filled has been released: no commit is on its way to its barriers
+      for (int i = 0; i < C::STAGES && ok; ++i) {
+        if (!mbar_wait(EMPTY(s), ph ^ 1u, a.status)) break;
+        if (++s == C::STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {  // ---------------- MMA issuer
+      constexpr uint32_t idesc = idesc_16<T>(256, BN);
+      int s = 0, it = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = cid; tile < num_tiles && ok; tile += nclusters) {
+        for (int kb0 = 0; kb0 < kblocks && ok; kb0 += chunk, ++it) {
+          if (!mbar_wait(TEMPTY(it & 1), ((it >> 1) & 1) ^ 1u, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t dt = tmem_base + (it & 1) * 256;
+          const int kb1 = min(kb0 + chunk, kblocks);
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(FULL(s), ph, a.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_pair(dt, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sb + k * 32), idesc, kb > kb0 || k > 0 ? 1u : 0u);
+            mma_commit_pair(EMPTY(s));
+            mma_commit_pair(mapa_shared(EMPTY(s), 1));
+            if (++s == C::STAGES) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+          if (ok) {
+            mma_commit_pair(TFULL(it & 1));
+            mma_commit_pair(mapa_shared(TFULL(it & 1), 1));
+          }
+        }
+      }
+      // every epilogue release, the partner's remote arrivals among them, has landed
+      for (int i = it >= 2 ? it - 2 : 0; i < it && ok; ++i)
+        if (!mbar_wait(TEMPTY(i & 1), (i >> 1) & 1, a.status)) break;
+    }
+  } else {  // ------------------------ epilogue warps 2..9 (both CTAs)
+    const int q = warp & 3, w = warp - 2, half = w >> 2;
+    const uint32_t buf0 = staging + w * 2 * C::BUF;
+    const uint32_t row = static_cast<uint32_t>(lane) * 128, r7 = lane & 7;
+    const bool res_tma = tma_out && a.residual != nullptr;
+    int it = 0, use = 0;  // accumulators read; staging tiles used
+    bool ok = true;
+    for (int tile = cid; tile < num_tiles && ok; tile += nclusters) {
+      const int m0 = (tile % m_tiles) * 256 + 128 * rank + 32 * q, n0 = (tile / m_tiles) * BN + half * C::COLS;
+      const int nchunks = m0 < a.M && n0 < a.N ? min(C::CHUNKS, (a.N - n0 + C::CW - 1) / C::CW) : 0;
+      // residual of chunk c into the staging tile of that chunk's use
+      auto load_residual = [&](int c) {
+        if (lane == 0) {
+          bulk_wait_read_all();  // what was staged there has been stored
+          const int b = (use + c) & 1;
+          mbar_arrive_expect_tx(RES(w, b), C::BUF);
+          tma_load_2d(buf0 + b * C::BUF, &tmR, RES(w, b), n0 + c * C::CW, m0);
+        }
+      };
+      if (res_tma)
+        for (int c = 0; c < 2 && c < nchunks; ++c) load_residual(c);
+      // 16-bit outputs read the accumulator piece by piece below; float32 sums are taken over here
+      float acc[F32 ? C::COLS : 1];
+      const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * C::COLS;
+      if constexpr (F32) {
+        for (int kb0 = 0; kb0 < kblocks; kb0 += chunk, ++it) {
+          ok = mbar_wait(TFULL(it & 1), (it >> 1) & 1, a.status);
+          __syncwarp();
+          if (__any_sync(0xffffffffu, !ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < C::COLS; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(tq + (it & 1) * 256 + c, r);
+            tmem_ld_wait<32>(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              acc[c + i] = kb0 == 0 ? __uint_as_float(r[i]) : acc[c + i] + __uint_as_float(r[i]);
+          }
+          tc_fence_before();
+          mbar_arrive_cluster(mapa_shared(TEMPTY(it & 1), 0));
+        }
+      } else {
+        ok = mbar_wait(TFULL(it & 1), (it >> 1) & 1, a.status);
+        __syncwarp();
+        ok = !__any_sync(0xffffffffu, !ok);
+        tc_fence_after();
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int c = 0; c < C::CHUNKS; ++c) {
+        if (c >= nchunks) break;
+        const int n = n0 + c * C::CW, b = use & 1;
+        const uint32_t buf = buf0 + b * C::BUF;
+        float v[C::CW];
+        if constexpr (F32) {
+#pragma unroll
+          for (int i = 0; i < C::CW; ++i) v[i] = acc[c * C::CW + i];
+        } else {
+          uint32_t* r = reinterpret_cast<uint32_t*>(v);
+          tmem_ld32(tq + (it & 1) * 256 + c * C::CW, r);
+          tmem_ld32(tq + (it & 1) * 256 + c * C::CW + 32, r + 32);
+          tmem_ld_wait<C::CW>(*reinterpret_cast<uint32_t(*)[C::CW]>(r));
+          if (c + 1 >= nchunks) {  // the last read of this accumulator
+            tc_fence_before();
+            mbar_arrive_cluster(mapa_shared(TEMPTY(it & 1), 0));
+          }
+        }
+        add_bias<C::CW>(a, n, v);
+        with_act(a.act, [&](auto act) {
+#pragma unroll
+          for (int i = 0; i < C::CW; ++i) v[i] = activate<decltype(act)::value>(v[i]);
+        });
+        if (tma_out) {
+          if (res_tma) {
+            ok = mbar_wait(RES(w, b), (use >> 1) & 1, a.status);
+            __syncwarp();
+            if (__any_sync(0xffffffffu, !ok)) {
+              ok = false;
+              break;
+            }
+          } else if (use >= 2) {  // the store two uses ago has read this tile
+            if (lane == 0) bulk_wait_read_but1();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint32_t at = buf + row + ((u ^ r7) << 4);
+            uint32_t p[4];
+            if (res_tma) {
+              const uint4 rr = ld_shared_v4(at);
+              p[0] = rr.x, p[1] = rr.y, p[2] = rr.z, p[3] = rr.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (F32) {
+                float z = v[4 * u + i];
+                if (res_tma) z += __uint_as_float(p[i]);
+                p[i] = __float_as_uint(z);
+              } else {
+                float z0 = v[8 * u + 2 * i], z1 = v[8 * u + 2 * i + 1];
+                if (res_tma) {
+                  const float2 rr = unpack2<T>(p[i]);
+                  z0 += rr.x;
+                  z1 += rr.y;
+                }
+                p[i] = pack2<T>(z0, z1);
+              }
+            }
+            st_shared_v4(at, p[0], p[1], p[2], p[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmY, buf, n, m0);  // rows past M and columns past N are clipped
+            bulk_commit_group();
+          }
+          if (res_tma && c + 2 < nchunks) load_residual(2);  // use + 2: the same tile, once stored
+        } else {
+          // 32 float32 columns at a time through the staging tile, then a row per step: lane = column
+#pragma unroll
+          for (int h = 0; h < C::CW; h += 32) {
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              st_shared_v4(buf + row + ((u ^ r7) << 4), __float_as_uint(v[h + 4 * u]), __float_as_uint(v[h + 4 * u + 1]),
+                           __float_as_uint(v[h + 4 * u + 2]), __float_as_uint(v[h + 4 * u + 3]));
+            __syncwarp();
+            const int nn = n + h + lane, rows = min(32, a.M - m0);
+            const uint8_t* src = smem + (buf - sbase);
+            if (nn < a.N) {
+#pragma unroll 8
+              for (int r = 0; r < rows; ++r)
+                linear_put<T, F32>(a, m0 + r, nn,
+                                   *reinterpret_cast<const float*>(src + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4));
+            }
+          }
+        }
+        ++use;
+      }
+      if (!F32) {
+        if (nchunks == 0) {
+          tc_fence_before();
+          mbar_arrive_cluster(mapa_shared(TEMPTY(it & 1), 0));
+        }
+        ++it;
+      }
+    }
+    if (lane == 0) bulk_wait_all();  // this warp's stores are complete
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();  // no CTA leaves while its partner may still signal it or use its TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+static bool map_rows(CUtensorMap* m, int dtype, const void* p, long long rows, long long cols, long long ld, int box_rows,
+                     int box_cols) {
+  const uint64_t es = dtype == DIT_DTYPE_F32 ? 4 : 2;
+  // one row has no stride; any aligned one will do
+  const uint64_t stride = rows > 1 ? ld * es : (cols * es + 15) / 16 * 16;
+  const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)}, strides[1] = {stride};
+  const uint32_t box[2] = {static_cast<uint32_t>(box_cols), static_cast<uint32_t>(box_rows)};
+  if (rows > 1 && ld < cols) return false;
+  return make_tmap_view(m, dtype, p, 2, dims, strides, box);
+}
+
+template <int BN, typename T, bool F32>
+static cudaError_t launch_pair(const LinearArgs& a, const CUtensorMap& tx, const CUtensorMap& tw, int num_sms,
+                               cudaStream_t st) {
+  using C = PairCfg<BN, F32>;
+  auto kernel = linear_pair_kernel<BN, T, F32>;
+  static int clusters_of[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(320);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {2, 1, 1};
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  if (clusters_of[dev] == 0) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(2 * (num_sms / 2));
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n <= 0) return cudaErrorInvalidConfiguration;
+    clusters_of[dev] = n < num_sms / 2 ? n : num_sms / 2;
+  }
+  const int od = F32 ? DIT_DTYPE_F32 : a.fp16 ? DIT_DTYPE_FP16 : DIT_DTYPE_BF16;
+  CUtensorMap ty = tx, tr = tx;
+  int tma_out = map_rows(&ty, od, a.y, a.M, a.N, a.ldy, 32, C::CW);
+  if (tma_out && a.residual) tma_out = map_rows(&tr, od, a.residual, a.M, a.N, a.ldr, 32, C::CW);
+  const long long tiles = static_cast<long long>((a.M + 255) / 256) * ((a.N + BN - 1) / BN);
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < clusters_of[dev] ? tiles : clusters_of[dev]));
+  cfg.numAttrs = g_pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tx, tw, tr, ty, a, tma_out);
+}
+
+// ------------------------------------------------------------------------- split K in a cluster
+template <int BN>
+struct SplitCfg {
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 96 * 1024 / STAGE;   // two CTAs per SM
+  static constexpr int ROW = BN + 4;                 // floats per partial row: 16-byte units of neighbouring rows in other banks
+  static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
+  static constexpr int TMEM = 2 * BN;                // two accumulators (chunks of a float32 sum)
+  static_assert(128 * ROW * 4 <= STAGES * STAGE, "the partial tile reuses the stages");
+};
+
+// 128 bytes (64 values) of `rows` rows from p (row r0, column k0) into a 128-byte-swizzled tile,
+// by 128 threads; values outside [R, K] are zero
+template <typename T>
+__device__ __forceinline__ void gather_tile(uint8_t* dst, const T* p, long long ld, int r0, int R, int k0, int K, int rows,
+                                            int grain, int tid) {
+  for (int i0 = tid; i0 < rows * 8; i0 += 128 * 4) {
+    uint32_t v[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * 128, r = i >> 3, k = k0 + (i & 7) * 8;
+      v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
+      if (i >= rows * 8 || r0 + r >= R || k >= K) continue;
+      const T* src = p + (r0 + r) * ld + k;
+      if (grain == 8 && k + 8 <= K) {
+        const uint2 a = *reinterpret_cast<const uint2*>(src), b = *reinterpret_cast<const uint2*>(src + 4);
+        v[j][0] = a.x, v[j][1] = a.y, v[j][2] = b.x, v[j][3] = b.y;
+      } else if (grain >= 4 && k + 8 <= K) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[j][e] = reinterpret_cast<const uint32_t*>(src)[e];
+      } else {
+        const uint16_t* s = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (k + e < K) v[j][e >> 1] |= static_cast<uint32_t>(s[e]) << (16 * (e & 1));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * 128, r = i >> 3, u = i & 7;
+      if (i < rows * 8)
+        *reinterpret_cast<uint4*>(dst + r * 128 + ((u ^ (r & 7)) << 4)) = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
+    }
+  }
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+struct SplitArgs {
+  int split;            // CTAs per cluster: K slices of a tile
+  int grain_x, grain_w; // 0: by TMA; else bytes that its rows are aligned to (2, 4 or 8)
+  int vec;              // y and residual rows allow four values at a time
+};
+
+template <int BN, typename T, bool GATHER>
+__global__ void __launch_bounds__(192)
+    linear_split_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                        const LinearArgs a, const SplitArgs sp, const int box_rows) {
+  using C = SplitCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem), bar0 = sbase + C::STAGES * C::STAGE;
+  auto FULL = [&](int s) { return bar0 + 8u * s; };
+  auto EMPTY = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+  auto TFULL = [&](int i) { return bar0 + 8u * (2 * C::STAGES + i); };
+  auto TEMPTY = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 2 + i); };
+  const uint32_t drain = bar0 + 8u * (2 * C::STAGES + 4);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::STAGES * C::STAGE + 8 * (2 * C::STAGES + 5));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int m_tiles = (a.M + 127) / 128;
+  const int tile = blockIdx.x / sp.split;
+  const int m0 = (tile % m_tiles) * 128, n0 = (tile / m_tiles) * BN;
+  const int kblocks_all = (a.K + 63) / 64;
+  const int kb_begin = static_cast<int>(static_cast<long long>(kblocks_all) * rank / sp.split);
+  const int kb_end = static_cast<int>(static_cast<long long>(kblocks_all) * (rank + 1) / sp.split);
+  const int chunk = a.out_f32 ? kF32ChunkBlocks : kblocks_all;
+  const int gathered = GATHER ? (sp.grain_x != 0) + (sp.grain_w != 0) : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(FULL(s), (gathered < 2 ? 1 : 0) + (gathered > 0 ? 128 : 0));
+      mbar_init(EMPTY(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(TFULL(i), 1);
+      mbar_init(TEMPTY(i), 128);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(holder), C::TMEM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *holder;
+  pdl_trigger();
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0 && gathered < 2) {  // ---------------- TMA loads
+      int s = 0;
+      uint32_t ph = 0, armed = 0;
+      bool ok = true;
+      const bool bx = !GATHER || sp.grain_x == 0, bw = !GATHER || sp.grain_w == 0;
+      for (int kb = kb_begin; kb < kb_end; ++kb) {
+        if (!mbar_wait(EMPTY(s), ph ^ 1u, a.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = sbase + s * C::STAGE;
+        mbar_arrive_expect_tx(FULL(s), (bx ? box_rows * 128 : 0) + (bw ? C::B_BYTES : 0));
+        // rows of the tile past box_rows keep what they held: they only reach rows past M
+        if (bx) tma_load_2d(sa, &tmX, FULL(s), kb * 64, m0);
+        if (bw) tma_load_2d(sa + C::A_BYTES, &tmW, FULL(s), kb * 64, n0);
+        armed |= 1u << s;
+        if (++s == C::STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok)  // a wait ran out: let the copies that were issued land before leaving
+        for (int j = 0; j < C::STAGES; ++j)
+          if (armed & (1u << j)) mbar_wait(FULL(j), j < s ? ph : ph ^ 1u, a.status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {  // ---------------- MMA issuer
+      constexpr uint32_t idesc = idesc_16<T>(128, BN);
+      int s = 0, it = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int kb0 = kb_begin; kb0 < kb_end && ok; kb0 += chunk, ++it) {
+        if (!mbar_wait(TEMPTY(it & 1), ((it >> 1) & 1) ^ 1u, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int kb1 = min(kb0 + chunk, kb_end);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(FULL(s), ph, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_ss(tmem_base + (it & 1) * BN, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sb + k * 32), idesc,
+                        kb > kb0 || k > 0 ? 1u : 0u);
+          mma_commit(EMPTY(s));
+          if (++s == C::STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) mma_commit(TFULL(it & 1));
+      }
+      if (!ok) {  // the MMAs that were issued finish before TMEM is freed
+        mma_commit(drain);
+        mbar_wait(drain, 0, a.status);
+      }
+    }
+  } else {  // ------------------------ warps 2..5: gather, then the sums of one row per thread
+    const int tid = threadIdx.x - 64, q = warp & 3, r = q * 32 + lane;
+    bool ok = true;
+    int s = 0, it = 0;
+    uint32_t ph = 0;
+    float acc[BN];
+#pragma unroll
+    for (int i = 0; i < BN; ++i) acc[i] = 0.f;
+    for (int kb0 = kb_begin; kb0 < kb_end && ok; kb0 += chunk, ++it) {
+      if (GATHER && gathered > 0) {
+        const int kb1 = min(kb0 + chunk, kb_end);
+        for (int kb = kb0; kb < kb1 && ok; ++kb) {
+          ok = mbar_wait(EMPTY(s), ph ^ 1u, a.status);
+          if (!ok) break;
+          uint8_t* sa = smem + s * C::STAGE;
+          if (sp.grain_x)
+            gather_tile(sa, static_cast<const T*>(a.x), a.ldx, m0, a.M, kb * 64, a.K, 128, sp.grain_x, tid);
+          if (sp.grain_w)
+            gather_tile(sa + C::A_BYTES, static_cast<const T*>(a.w), a.ldw, n0, a.N, kb * 64, a.K, BN, sp.grain_w, tid);
+          fence_proxy_async_smem();
+          mbar_arrive(FULL(s));
+          if (++s == C::STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (ok) ok = mbar_wait(TFULL(it & 1), (it >> 1) & 1, a.status);
+      __syncwarp();
+      if (__any_sync(0xffffffffu, !ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < BN; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (it & 1) * BN + c, v);
+        tmem_ld_wait<32>(v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[c + i] += __uint_as_float(v[i]);
+      }
+      tc_fence_before();
+      mbar_arrive(TEMPTY(it & 1));
+    }
+    // the last accumulator is full: every stage has been read, and the partial tile takes their place
+    if (ok && m0 + r < a.M) {
+#pragma unroll
+      for (int c = 0; c < BN; c += 4)
+        *reinterpret_cast<float4*>(smem + (r * C::ROW + c) * 4) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();  // the partial tiles of all slices are written
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM);
+  }
+  // this CTA's share of the tile, four columns per thread and step, slices added in their order
+  const int rows = min(128, a.M - m0), total = rows * (BN / 4);
+  for (int i = rank * 192 + static_cast<int>(threadIdx.x); i < total; i += 192 * sp.split) {
+    const int r = i / (BN / 4), c = (i % (BN / 4)) * 4, m = m0 + r, n = n0 + c;
+    if (n >= a.N) continue;
+    const uint32_t at = sbase + (r * C::ROW + c) * 4;
+    float v[4] = {};
+    for (int j = 0; j < sp.split; ++j) {
+      const float4 p = ld_cluster_f4(mapa_shared(at, j));
+      v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+    }
+    add_bias<4>(a, n, v);
+    with_act(a.act, [&](auto act) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = activate<decltype(act)::value>(v[e]);
+    });
+    if (sp.vec && n + 4 <= a.N) {
+      if (a.out_f32) {
+        if (a.residual) {
+          const float4 p = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + m * a.ldr + n);
+          v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+        }
+        *reinterpret_cast<float4*>(static_cast<float*>(a.y) + m * a.ldy + n) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+        if (a.residual) {
+          const uint2 p = *reinterpret_cast<const uint2*>(static_cast<const T*>(a.residual) + m * a.ldr + n);
+          const float2 u = unpack2<T>(p.x), w = unpack2<T>(p.y);
+          v[0] += u.x, v[1] += u.y, v[2] += w.x, v[3] += w.y;
+        }
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.y) + m * a.ldy + n) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < a.N) {
+          if (a.out_f32) linear_put<T, true>(a, m, n + e, v[e]);
+          else linear_put<T, false>(a, m, n + e, v[e]);
+        }
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();  // no CTA leaves while another reads its partial tile
+}
+
+template <int BN, typename T, bool GATHER>
+static cudaError_t launch_split(const LinearArgs& a, const CUtensorMap& tx, const CUtensorMap& tw, SplitArgs sp,
+                                int box_rows, cudaStream_t st) {
+  using C = SplitCfg<BN>;
+  auto kernel = linear_split_kernel<BN, T, GATHER>;
+  static bool set[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    set[dev] = true;
+  }
+  const long long ctas = static_cast<long long>((a.M + 127) / 128) * ((a.N + BN - 1) / BN) * sp.split;
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {static_cast<unsigned>(sp.split), 1, 1};
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = g_pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a, sp, box_rows);
+}
+
+template <typename T>
+static cudaError_t launch_tc(const LinearArgs& a, int num_sms, cudaStream_t st) {
+  const int dt = a.fp16 ? DIT_DTYPE_FP16 : DIT_DTYPE_BF16;
+  const int kblocks = (a.K + 63) / 64;
+  CUtensorMap tx, tw;
+  const long long tiles256 = static_cast<long long>((a.M + 255) / 256) * ((a.N + 255) / 256);
+  const long long tiles128 = static_cast<long long>((a.M + 255) / 256) * ((a.N + 127) / 128);
+  if (tiles128 >= num_sms / 2 && map_rows(&tx, dt, a.x, a.M, a.K, a.ldx, 128, 64)) {
+    const bool wide = !a.out_f32 && tiles256 >= num_sms / 2;
+    if (map_rows(&tw, dt, a.w, a.N, a.K, a.ldw, wide ? 128 : 64, 64)) {
+      if (a.out_f32) return launch_pair<128, T, true>(a, tx, tw, num_sms, st);
+      return wide ? launch_pair<256, T, false>(a, tx, tw, num_sms, st) : launch_pair<128, T, false>(a, tx, tw, num_sms, st);
+    }
+  }
+  // the split kernel
+  auto grain = [](const void* p, long long ld) {
+    const uintptr_t v = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * 2);
+    return v % 8 == 0 ? 8 : v % 4 == 0 ? 4 : 2;
+  };
+  SplitArgs sp;
+  const long long mt = (a.M + 127) / 128;
+  const bool narrow = mt * ((a.N + 127) / 128) < num_sms;
+  const int bn = narrow ? 64 : 128;
+  const long long tiles = mt * ((a.N + bn - 1) / bn);
+  sp.split = 1;
+  while (sp.split < 8 && tiles * sp.split * 2 <= 2 * num_sms && kblocks >= 4 * sp.split) sp.split *= 2;
+  const int box_rows = a.M >= 128 ? 128 : (a.M + 7) / 8 * 8;
+  sp.grain_x = map_rows(&tx, dt, a.x, a.M, a.K, a.ldx, box_rows, 64) ? 0 : grain(a.x, a.ldx);
+  sp.grain_w = map_rows(&tw, dt, a.w, a.N, a.K, a.ldw, bn, 64) ? 0 : grain(a.w, a.ldw);
+  const int es = a.out_f32 ? 4 : 2;
+  auto four = [&](const void* p, long long ld) {
+    return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * es)) & (4 * es - 1)) == 0;
+  };
+  sp.vec = four(a.y, a.ldy) && (a.residual == nullptr || four(a.residual, a.ldr));
+  if (sp.grain_x && sp.grain_w) tx = tw = CUtensorMap{};
+  else if (sp.grain_x) tx = tw;
+  else if (sp.grain_w) tw = tx;
+  const bool gather = sp.grain_x || sp.grain_w;
+  if (narrow)
+    return gather ? launch_split<64, T, true>(a, tx, tw, sp, box_rows, st)
+                  : launch_split<64, T, false>(a, tx, tw, sp, box_rows, st);
+  return gather ? launch_split<128, T, true>(a, tx, tw, sp, box_rows, st)
+                : launch_split<128, T, false>(a, tx, tw, sp, box_rows, st);
+}
+
+cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t st) {
+  return a.fp16 ? launch_tc<__half>(a, num_sms, st) : launch_tc<__nv_bfloat16>(a, num_sms, st);
+}
+
+}  // namespace dit

@@ -3,6 +3,7 @@
 // rotary positions.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -24,6 +25,8 @@ struct LinearArgs {
   int* status;
 };
 cudaError_t launch_linear_fused(const LinearArgs& a, int num_sms, cudaStream_t st);
+// The tensor-core kernels (op_linear_tc.cu).
+cudaError_t launch_linear_tc(const LinearArgs& a, int num_sms, cudaStream_t st);
 
 // Packed attention: sequence s owns query tokens cu_q[s] .. cu_q[s+1] and keys cu_k[s] .. cu_k[s+1].
 struct PackedAttnArgs {
@@ -48,5 +51,10 @@ struct RotaryArgs {
   int dtype, pos64, interleaved, transpose;
 };
 cudaError_t launch_rotary(const dit_rotary& r, const RotaryArgs& a, int num_sms, cudaStream_t st);
+
+// Tensor map of a strided view: dims[0] contiguous, strides_bytes[i] from dims[i] to dims[i+1],
+// box[0] 128 bytes wide, 128-byte swizzle.  False where TMA cannot read it.
+bool make_tmap_view(CUtensorMap* map, int dtype, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides_bytes, const uint32_t* box);
 
 }  // namespace dit
