@@ -41,4 +41,22 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// One lane of a converged warp, the same each time.  The roles that issue TMA copies and MMAs
+// run their loops with the whole warp and elect a lane around the instructions alone: their
+// operands then stay warp-uniform.  With the loop inside `if (lane == 0)` the four MMAs and the
+// commit of one K stage took 543 cycles to issue (clock64), whatever their size.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e != 0;
+}
+// mbar_wait by a whole warp: false for every lane when it ran out for any
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+}
+
 }  // namespace dit

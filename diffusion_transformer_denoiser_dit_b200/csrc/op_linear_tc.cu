@@ -3,15 +3,15 @@
 // linear_pair_kernel: 256 x BN output tiles on SM pairs (tcgen05 cta_group::2), persistent.
 //   A pair moves 256 + BN operand rows per 256 x BN x 64 multiply-adds, half of what two single
 //   SMs would.  Warp 0 of each CTA loads its 128 rows of x and BN/2 rows of W per 64-wide K
-//   stage by TMA; one thread of the leader issues the MMAs of both SMs; warps 2-9 of each CTA
+//   stage by TMA; one thread of the leader issues the MMAs of both SMs; warps 4-11 of each CTA
 //   finish 32 rows x BN/2 columns each.  Two accumulators in TMEM: the epilogue of one tile
 //   runs beside the main loop of the next.  The residual is loaded by TMA into the staging
 //   tile while the main loop still runs, added there, and stored from there by TMA.
 //
 // linear_split_kernel: 128 x BN tiles, one CTA per tile and K slice; the CTAs of a cluster hold
-//   the slices of one tile, leave their float32 partial tiles in shared memory, and each adds up
-//   and finishes its share of the tile from all of them over distributed shared memory, in the
-//   order of the slices, so that results repeat bit for bit.  For products with too few 256-row
+//   the slices of one tile, send each row of their float32 partial tiles to the CTA that finishes
+//   that row (distributed shared memory), and each adds up its rows in the order of the slices,
+//   so that results repeat bit for bit.  For products with too few 256-row
 //   tiles to fill the GPU.  Operands whose rows do not start on 16-byte boundaries are copied
 //   into shared memory by the epilogue warps instead of TMA (GATHER).
 //
@@ -72,17 +72,28 @@ struct PairCfg {
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, STAGE = A_BYTES + B_BYTES;
   static constexpr int COLS = BN / 2;             // columns per epilogue warp
   static constexpr int CW = F32 ? 32 : 64;        // columns per 128-byte staging row
-  static constexpr int CHUNKS = COLS / CW;
+  static constexpr int CHUNKS = F32 ? COLS / CW : 2;  // at most, per epilogue warp
   static constexpr int BUF = 32 * 128;            // one staging tile: 32 rows of 128 bytes
   static constexpr int STAGING = 8 * 2 * BUF;
   static constexpr int FIT = (232448 - 1024 - 512 - STAGING) / STAGE;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM = 1024 + STAGES * STAGE + STAGING + 512;
-  static_assert(STAGES >= 4 && B_BYTES % 1024 == 0 && CHUNKS >= 1, "tile shape");
+  static constexpr int THREADS = 384;             // warpgroup 0: loads, MMA; 1, 2: epilogue
+  static constexpr int REG_CTRL = 80, REG_EPI = 208;
+  static constexpr int REG_POOL = 128 * REG_CTRL + 256 * REG_EPI;  // must fit the launch allocation
+  static_assert(STAGES >= 4 && B_BYTES % 1024 == 0 && COLS % 32 == 0, "tile shape");
 };
 
+// Tiles in groups of 8 tile rows, columns outermost inside a group: the tiles that run at one
+// time are a block of the output, whose rows of x and W stay in L2 between their uses.
+__device__ __forceinline__ void tile_at(int tile, int m_tiles, int n_tiles, int& mt, int& nt) {
+  const int per = 8 * n_tiles, g = tile / per, left = tile - g * per, h = min(8, m_tiles - 8 * g);
+  nt = left / h;
+  mt = 8 * g + left - nt * h;
+}
+
 template <int BN, typename T, bool F32>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(384, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmY,
                        const LinearArgs a, const int tma_out) {
@@ -137,22 +148,28 @@ __global__ void __launch_bounds__(320, 1)
   pdl_trigger();
   pdl_wait();
 
-  if (warp == 0) {
-    if (lane == 0) {  // ---------------- loads (both CTAs)
+  if (warp < 4) {
+    regs_dec<C::REG_CTRL>();
+    if (warp == 0) {  // ---------------- loads (both CTAs)
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int tile = cid; tile < num_tiles && ok; tile += nclusters) {
-        const int m0 = (tile % m_tiles) * 256 + 128 * rank, n0 = (tile / m_tiles) * BN + BN / 2 * rank;
+        int mt, nt;
+        tile_at(tile, m_tiles, n_tiles, mt, nt);
+        const int m0 = mt * 256 + 128 * rank, n0 = nt * BN + BN / 2 * rank;
         for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(EMPTY(s), ph ^ 1u, a.status)) {
+          if (!mbar_wait_warp(EMPTY(s), ph ^ 1u, a.status)) {
             ok = false;
             break;
           }
           const uint32_t sa = sbase + s * C::STAGE, full = mapa_shared(FULL(s), 0);
-          if (leader) mbar_arrive_expect_tx(FULL(s), 2 * C::STAGE);
-          tma_load_2d_pair(sa, &tmX, full, kb * 64, m0);
-          tma_load_2d_pair(sa + C::A_BYTES, &tmW, full, kb * 64, n0);
+          if (elect_one()) {
+            if (leader) mbar_arrive_expect_tx(FULL(s), 2 * C::STAGE);
+            tma_load_2d_pair(sa, &tmX, full, kb * 64, m0);
+            tma_load_2d_pair(sa + C::A_BYTES, &tmW, full, kb * 64, n0);
+          }
+          __syncwarp();
           if (++s == C::STAGES) {
             s = 0;
             ph ^= 1u;
@@ -161,22 +178,20 @@ __global__ void __launch_bounds__(320, 1)
       }
       // every stage this CTA filled has been released: no commit is on its way to its barriers
       for (int i = 0; i < C::STAGES && ok; ++i) {
-        if (!mbar_wait(EMPTY(s), ph ^ 1u, a.status)) break;
+        if (!mbar_wait_warp(EMPTY(s), ph ^ 1u, a.status)) break;
         if (++s == C::STAGES) {
           s = 0;
           ph ^= 1u;
         }
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {  // ---------------- MMA issuer
+    } else if (warp == 1 && leader) {  // ---------------- MMA issuer
       constexpr uint32_t idesc = idesc_16<T>(256, BN);
       int s = 0, it = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int tile = cid; tile < num_tiles && ok; tile += nclusters) {
         for (int kb0 = 0; kb0 < kblocks && ok; kb0 += chunk, ++it) {
-          if (!mbar_wait(TEMPTY(it & 1), ((it >> 1) & 1) ^ 1u, a.status)) {
+          if (!mbar_wait_warp(TEMPTY(it & 1), ((it >> 1) & 1) ^ 1u, a.status)) {
             ok = false;
             break;
           }
@@ -184,56 +199,72 @@ __global__ void __launch_bounds__(320, 1)
           const uint32_t dt = tmem_base + (it & 1) * 256;
           const int kb1 = min(kb0 + chunk, kblocks);
           for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(FULL(s), ph, a.status)) {
+            if (!mbar_wait_warp(FULL(s), ph, a.status)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16_pair(dt, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sb + k * 32), idesc, kb > kb0 || k > 0 ? 1u : 0u);
-            mma_commit_pair(EMPTY(s));
-            mma_commit_pair(mapa_shared(EMPTY(s), 1));
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_pair(dt, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sb + k * 32), idesc, kb > kb0 || k > 0 ? 1u : 0u);
+              mma_commit_pair(EMPTY(s));
+              mma_commit_pair(mapa_shared(EMPTY(s), 1));
+            }
+            __syncwarp();
             if (++s == C::STAGES) {
               s = 0;
               ph ^= 1u;
             }
           }
-          if (ok) {
+          if (ok && elect_one()) {
             mma_commit_pair(TFULL(it & 1));
             mma_commit_pair(mapa_shared(TFULL(it & 1), 1));
           }
+          __syncwarp();
         }
       }
       // every epilogue release, the partner's remote arrivals among them, has landed
       for (int i = it >= 2 ? it - 2 : 0; i < it && ok; ++i)
-        if (!mbar_wait(TEMPTY(i & 1), (i >> 1) & 1, a.status)) break;
+        if (!mbar_wait_warp(TEMPTY(i & 1), (i >> 1) & 1, a.status)) break;
     }
-  } else {  // ------------------------ epilogue warps 2..9 (both CTAs)
-    const int q = warp & 3, w = warp - 2, half = w >> 2;
+  } else {  // ------------------------ epilogue warps 4..11 (both CTAs)
+    regs_inc<C::REG_EPI>();
+    const int q = warp & 3, w = warp - 4, half = w >> 2;
     const uint32_t buf0 = staging + w * 2 * C::BUF;
     const uint32_t row = static_cast<uint32_t>(lane) * 128, r7 = lane & 7;
     const bool res_tma = tma_out && a.residual != nullptr;
-    int it = 0, use = 0;  // accumulators read; staging tiles used
+    int it = 0, use = 0, turn = 0;  // accumulators read; staging tiles used; tiles
     bool ok = true;
     for (int tile = cid; tile < num_tiles && ok; tile += nclusters) {
-      const int m0 = (tile % m_tiles) * 256 + 128 * rank + 32 * q, n0 = (tile / m_tiles) * BN + half * C::COLS;
-      const int nchunks = m0 < a.M && n0 < a.N ? min(C::CHUNKS, (a.N - n0 + C::CW - 1) / C::CW) : 0;
+      int mt, nt;
+      tile_at(tile, m_tiles, n_tiles, mt, nt);
+      const int m0 = mt * 256 + 128 * rank + 32 * q, n0 = nt * BN;
+      // chunk c of this warp starts at tile column col(c): a half of contiguous float32 chunks, or
+      // every other 64-wide chunk (of three, two or one, the two halves taking turns by tile)
+      const int hh = half ^ (BN % 128 != 0 ? turn & 1 : 0);
+      ++turn;
+      auto col = [&](int c) { return F32 ? half * C::COLS + c * C::CW : 64 * (hh + 2 * c); };
+      int nchunks = 0;
+      if (m0 < a.M)
+        for (int c = 0; c < C::CHUNKS; ++c) nchunks += col(c) < BN && n0 + col(c) < a.N;
       // residual of chunk c into the staging tile of that chunk's use
-      auto load_residual = [&](int c) {
+      auto load_residual = [&](int c, int ahead) {
         if (lane == 0) {
           bulk_wait_read_all();  // what was staged there has been stored
-          const int b = (use + c) & 1;
+          const int b = (use + ahead) & 1;
           mbar_arrive_expect_tx(RES(w, b), C::BUF);
-          tma_load_2d(buf0 + b * C::BUF, &tmR, RES(w, b), n0 + c * C::CW, m0);
+          tma_load_2d(buf0 + b * C::BUF, &tmR, RES(w, b), n0 + col(c), m0);
         }
       };
       if (res_tma)
-        for (int c = 0; c < 2 && c < nchunks; ++c) load_residual(c);
+        for (int c = 0; c < 2 && c < nchunks; ++c) load_residual(c, c);
       // 16-bit outputs read the accumulator piece by piece below; float32 sums are taken over here
       float acc[F32 ? C::COLS : 1];
-      const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * C::COLS;
+#pragma unroll
+      for (int i = 0; i < (F32 ? C::COLS : 1); ++i) acc[i] = 0.f;
+      const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
       if constexpr (F32) {
         for (int kb0 = 0; kb0 < kblocks; kb0 += chunk, ++it) {
           ok = mbar_wait(TFULL(it & 1), (it >> 1) & 1, a.status);
@@ -244,13 +275,12 @@ __global__ void __launch_bounds__(320, 1)
           }
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < C::COLS; c += 32) {
-            uint32_t r[32];
-            tmem_ld32(tq + (it & 1) * 256 + c, r);
-            tmem_ld_wait<32>(r);
+          for (int c = 0; c < C::COLS; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(tq + (it & 1) * 256 + half * C::COLS + c, r);
+            tmem_ld_wait<16>(r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              acc[c + i] = kb0 == 0 ? __uint_as_float(r[i]) : acc[c + i] + __uint_as_float(r[i]);
+            for (int i = 0; i < 16; ++i) acc[c + i] += __uint_as_float(r[i]);
           }
           tc_fence_before();
           mbar_arrive_cluster(mapa_shared(TEMPTY(it & 1), 0));
@@ -265,16 +295,14 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
       for (int c = 0; c < C::CHUNKS; ++c) {
         if (c >= nchunks) break;
-        const int n = n0 + c * C::CW, b = use & 1;
+        const int n = n0 + col(c), b = use & 1;
         const uint32_t buf = buf0 + b * C::BUF;
-        float v[C::CW];
-        if constexpr (F32) {
-#pragma unroll
-          for (int i = 0; i < C::CW; ++i) v[i] = acc[c * C::CW + i];
-        } else {
+        float own[F32 ? 1 : C::CW];
+        float* v = F32 ? acc + c * C::CW : own;  // registers: every index below is a constant
+        if constexpr (!F32) {
           uint32_t* r = reinterpret_cast<uint32_t*>(v);
-          tmem_ld32(tq + (it & 1) * 256 + c * C::CW, r);
-          tmem_ld32(tq + (it & 1) * 256 + c * C::CW + 32, r + 32);
+          tmem_ld32(tq + (it & 1) * 256 + col(c), r);
+          tmem_ld32(tq + (it & 1) * 256 + col(c) + 32, r + 32);
           tmem_ld_wait<C::CW>(*reinterpret_cast<uint32_t(*)[C::CW]>(r));
           if (c + 1 >= nchunks) {  // the last read of this accumulator
             tc_fence_before();
@@ -330,7 +358,7 @@ __global__ void __launch_bounds__(320, 1)
             tma_store_2d(&tmY, buf, n, m0);  // rows past M and columns past N are clipped
             bulk_commit_group();
           }
-          if (res_tma && c + 2 < nchunks) load_residual(2);  // use + 2: the same tile, once stored
+          if (res_tma && c + 2 < nchunks) load_residual(c + 2, 2);  // the same staging tile, once stored
         } else {
           // 32 float32 columns at a time through the staging tile, then a row per step: lane = column
 #pragma unroll
@@ -344,7 +372,7 @@ __global__ void __launch_bounds__(320, 1)
             const int nn = n + h + lane, rows = min(32, a.M - m0);
             const uint8_t* src = smem + (buf - sbase);
             if (nn < a.N) {
-#pragma unroll 8
+#pragma unroll 2
               for (int r = 0; r < rows; ++r)
                 linear_put<T, F32>(a, m0 + r, nn,
                                    *reinterpret_cast<const float*>(src + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4));
@@ -392,7 +420,7 @@ static cudaError_t launch_pair(const LinearArgs& a, const CUtensorMap& tx, const
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(320);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
@@ -404,6 +432,11 @@ static cudaError_t launch_pair(const LinearArgs& a, const CUtensorMap& tx, const
   if (clusters_of[dev] == 0) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
+    // the register split (setmaxnreg) must fit in the launch allocation, or it would wait forever
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * C::THREADS < C::REG_POOL) return cudaErrorInvalidConfiguration;
     cfg.gridDim = dim3(2 * (num_sms / 2));
     cfg.numAttrs = 1;
     int n = 0;
@@ -427,11 +460,16 @@ static cudaError_t launch_pair(const LinearArgs& a, const CUtensorMap& tx, const
 template <int BN>
 struct SplitCfg {
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 96 * 1024 / STAGE;   // two CTAs per SM
-  static constexpr int ROW = BN + 4;                 // floats per partial row: 16-byte units of neighbouring rows in other banks
-  static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
+  static constexpr int PART = 128 * BN * 4;          // partial rows of all slices for this CTA's share
+  // One CTA per SM with all of its memory in flight: a round trip of a stage (load, product,
+  // release) took 1.6 us measured, so 96 KB of stages fed an SM 31 bytes a cycle and no more.
+  static constexpr int STAGES = (232448 - 1024 - 256 - PART) / STAGE;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + PART + 256;
   static constexpr int TMEM = 2 * BN;                // two accumulators (chunks of a float32 sum)
-  static_assert(128 * ROW * 4 <= STAGES * STAGE, "the partial tile reuses the stages");
+  // 16-byte unit u of partial row r: rows 8 apart in one bank group, neighbours in others
+  static __device__ __forceinline__ uint32_t part_at(int r, int u) {
+    return static_cast<uint32_t>(r) * (BN * 4) + static_cast<uint32_t>((u & ~7) | ((u ^ r) & 7)) * 16;
+  }
 };
 
 // 128 bytes (64 values) of `rows` rows from p (row r0, column k0) into a 128-byte-swizzled tile,
@@ -469,10 +507,8 @@ __device__ __forceinline__ void gather_tile(uint8_t* dst, const T* p, long long 
   }
 }
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float x, float y, float z, float w) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 
 struct SplitArgs {
@@ -488,13 +524,13 @@ __global__ void __launch_bounds__(192)
   using C = SplitCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sbase = smem_u32(smem), bar0 = sbase + C::STAGES * C::STAGE;
+  const uint32_t sbase = smem_u32(smem), part = sbase + C::STAGES * C::STAGE, bar0 = part + C::PART;
   auto FULL = [&](int s) { return bar0 + 8u * s; };
   auto EMPTY = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
   auto TFULL = [&](int i) { return bar0 + 8u * (2 * C::STAGES + i); };
   auto TEMPTY = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 2 + i); };
   const uint32_t drain = bar0 + 8u * (2 * C::STAGES + 4);
-  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::STAGES * C::STAGE + 8 * (2 * C::STAGES + 5));
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::STAGES * C::STAGE + C::PART + 8 * (2 * C::STAGES + 5));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int m_tiles = (a.M + 127) / 128;
@@ -504,6 +540,8 @@ __global__ void __launch_bounds__(192)
   const int kb_begin = static_cast<int>(static_cast<long long>(kblocks_all) * rank / sp.split);
   const int kb_end = static_cast<int>(static_cast<long long>(kblocks_all) * (rank + 1) / sp.split);
   const int chunk = a.out_f32 ? kF32ChunkBlocks : kblocks_all;
+  // rows of the tile that one CTA of the cluster finishes
+  const int share = (min(128, a.M - m0) + sp.split - 1) / sp.split;
   const int gathered = GATHER ? (sp.grain_x != 0) + (sp.grain_w != 0) : 0;
 
   if (threadIdx.x == 0) {
@@ -530,21 +568,24 @@ __global__ void __launch_bounds__(192)
   pdl_wait();
 
   if (warp == 0) {
-    if (lane == 0 && gathered < 2) {  // ---------------- TMA loads
+    if (gathered < 2) {  // ---------------- TMA loads
       int s = 0;
       uint32_t ph = 0, armed = 0;
       bool ok = true;
       const bool bx = !GATHER || sp.grain_x == 0, bw = !GATHER || sp.grain_w == 0;
       for (int kb = kb_begin; kb < kb_end; ++kb) {
-        if (!mbar_wait(EMPTY(s), ph ^ 1u, a.status)) {
+        if (!mbar_wait_warp(EMPTY(s), ph ^ 1u, a.status)) {
           ok = false;
           break;
         }
         const uint32_t sa = sbase + s * C::STAGE;
-        mbar_arrive_expect_tx(FULL(s), (bx ? box_rows * 128 : 0) + (bw ? C::B_BYTES : 0));
-        // rows of the tile past box_rows keep what they held: they only reach rows past M
-        if (bx) tma_load_2d(sa, &tmX, FULL(s), kb * 64, m0);
-        if (bw) tma_load_2d(sa + C::A_BYTES, &tmW, FULL(s), kb * 64, n0);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(FULL(s), (bx ? box_rows * 128 : 0) + (bw ? C::B_BYTES : 0));
+          // rows of the tile past box_rows keep what they held: they only reach rows past M
+          if (bx) tma_load_2d(sa, &tmX, FULL(s), kb * 64, m0);
+          if (bw) tma_load_2d(sa + C::A_BYTES, &tmW, FULL(s), kb * 64, n0);
+        }
+        __syncwarp();
         armed |= 1u << s;
         if (++s == C::STAGES) {
           s = 0;
@@ -553,42 +594,47 @@ __global__ void __launch_bounds__(192)
       }
       if (!ok)  // a wait ran out: let the copies that were issued land before leaving
         for (int j = 0; j < C::STAGES; ++j)
-          if (armed & (1u << j)) mbar_wait(FULL(j), j < s ? ph : ph ^ 1u, a.status);
+          if (armed & (1u << j)) mbar_wait_warp(FULL(j), j < s ? ph : ph ^ 1u, a.status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {  // ---------------- MMA issuer
+    {  // ---------------- MMA issuer
       constexpr uint32_t idesc = idesc_16<T>(128, BN);
       int s = 0, it = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int kb0 = kb_begin; kb0 < kb_end && ok; kb0 += chunk, ++it) {
-        if (!mbar_wait(TEMPTY(it & 1), ((it >> 1) & 1) ^ 1u, a.status)) {
+        if (!mbar_wait_warp(TEMPTY(it & 1), ((it >> 1) & 1) ^ 1u, a.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const int kb1 = min(kb0 + chunk, kb_end);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(FULL(s), ph, a.status)) {
+          if (!mbar_wait_warp(FULL(s), ph, a.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16_ss(tmem_base + (it & 1) * BN, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sb + k * 32), idesc,
-                        kb > kb0 || k > 0 ? 1u : 0u);
-          mma_commit(EMPTY(s));
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_ss(tmem_base + (it & 1) * BN, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sb + k * 32), idesc,
+                          kb > kb0 || k > 0 ? 1u : 0u);
+            mma_commit(EMPTY(s));
+          }
+          __syncwarp();
           if (++s == C::STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
-        if (ok) mma_commit(TFULL(it & 1));
+        if (ok && elect_one()) mma_commit(TFULL(it & 1));
+        __syncwarp();
       }
       if (!ok) {  // the MMAs that were issued finish before TMEM is freed
-        mma_commit(drain);
+        if (elect_one()) mma_commit(drain);
+        __syncwarp();
         mbar_wait(drain, 0, a.status);
       }
     }
@@ -637,62 +683,95 @@ __global__ void __launch_bounds__(192)
       tc_fence_before();
       mbar_arrive(TEMPTY(it & 1));
     }
-    // the last accumulator is full: every stage has been read, and the partial tile takes their place
+    // row r goes to the CTA that finishes it: CTA r / share keeps rows share * CTA .. of the tile,
+    // slice after slice
     if (ok && m0 + r < a.M) {
+      const int owner = r / share;
+      const uint32_t base = mapa_shared(part, owner);
+      const int pr = rank * share + (r - owner * share);
 #pragma unroll
-      for (int c = 0; c < BN; c += 4)
-        *reinterpret_cast<float4*>(smem + (r * C::ROW + c) * 4) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+      for (int u = 0; u < BN / 4; ++u)
+        st_cluster_f4(base + C::part_at(pr, u), acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
     }
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync_all();  // the partial tiles of all slices are written
+  cluster_sync_all();  // the partial rows of all slices are where they are finished
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM);
   }
-  // this CTA's share of the tile, four columns per thread and step, slices added in their order
-  const int rows = min(128, a.M - m0), total = rows * (BN / 4);
-  for (int i = rank * 192 + static_cast<int>(threadIdx.x); i < total; i += 192 * sp.split) {
-    const int r = i / (BN / 4), c = (i % (BN / 4)) * 4, m = m0 + r, n = n0 + c;
-    if (n >= a.N) continue;
-    const uint32_t at = sbase + (r * C::ROW + c) * 4;
-    float v[4] = {};
-    for (int j = 0; j < sp.split; ++j) {
-      const float4 p = ld_cluster_f4(mapa_shared(at, j));
-      v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
-    }
-    add_bias<4>(a, n, v);
-    with_act(a.act, [&](auto act) {
+  // this CTA's rows: a thread keeps its four columns and steps through the rows, slices added in
+  // their order; four rows at a time, so that the loads of a batch are in flight together
+  constexpr int UNITS = BN / 4, STEP = 192 / UNITS;
+  static_assert(192 % UNITS == 0, "whole rows per step");
+  const int u = threadIdx.x % UNITS, n = n0 + 4 * u, r0 = m0 + rank * share, rows = min(share, a.M - r0);
+  if (n < a.N) {
+    float bias[4] = {};
+    add_bias<4>(a, n, bias);
+    const bool vec = sp.vec && n + 4 <= a.N;
+    for (int r = threadIdx.x / UNITS; r < rows; r += 4 * STEP) {
+      float v[4][4], res[4][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = activate<decltype(act)::value>(v[e]);
-    });
-    if (sp.vec && n + 4 <= a.N) {
-      if (a.out_f32) {
-        if (a.residual) {
-          const float4 p = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + m * a.ldr + n);
-          v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+      for (int k = 0; k < 4; ++k) {
+        const int rr = r + k * STEP;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = bias[e];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) res[k][e] = 0.f;
+        if (rr < rows && a.residual) {
+          const long long at = (r0 + rr) * a.ldr + n;
+          if (a.out_f32) {
+            const float* p = static_cast<const float*>(a.residual) + at;
+            if (vec) *reinterpret_cast<float4*>(res[k]) = *reinterpret_cast<const float4*>(p);
+            else
+              for (int e = 0; e < 4; ++e) res[k][e] = n + e < a.N ? p[e] : 0.f;
+          } else {
+            const T* p = static_cast<const T*>(a.residual) + at;
+            if (vec) {
+              const uint2 w = *reinterpret_cast<const uint2*>(p);
+              const float2 y0 = unpack2<T>(w.x), y1 = unpack2<T>(w.y);
+              res[k][0] = y0.x, res[k][1] = y0.y, res[k][2] = y1.x, res[k][3] = y1.y;
+            } else {
+              for (int e = 0; e < 4; ++e) res[k][e] = n + e < a.N ? to_f32(p[e]) : 0.f;
+            }
+          }
         }
-        *reinterpret_cast<float4*>(static_cast<float*>(a.y) + m * a.ldy + n) = make_float4(v[0], v[1], v[2], v[3]);
-      } else {
-        if (a.residual) {
-          const uint2 p = *reinterpret_cast<const uint2*>(static_cast<const T*>(a.residual) + m * a.ldr + n);
-          const float2 u = unpack2<T>(p.x), w = unpack2<T>(p.y);
-          v[0] += u.x, v[1] += u.y, v[2] += w.x, v[3] += w.y;
-        }
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.y) + m * a.ldy + n) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
       }
-    } else {
+      for (int j = 0; j < sp.split; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < a.N) {
-          if (a.out_f32) linear_put<T, true>(a, m, n + e, v[e]);
-          else linear_put<T, false>(a, m, n + e, v[e]);
+        for (int k = 0; k < 4; ++k) {
+          if (r + k * STEP >= rows) break;
+          const uint4 p = ld_shared_v4(part + C::part_at(j * share + r + k * STEP, u));
+          v[k][0] += __uint_as_float(p.x), v[k][1] += __uint_as_float(p.y);
+          v[k][2] += __uint_as_float(p.z), v[k][3] += __uint_as_float(p.w);
         }
+      with_act(a.act, [&](auto act) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[k][e] = activate<decltype(act)::value>(v[k][e]) + res[k][e];
+      });
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (r + k * STEP >= rows) break;
+        const long long at = (r0 + r + k * STEP) * a.ldy + n;
+        if (a.out_f32) {
+          float* p = static_cast<float*>(a.y) + at;
+          if (vec) *reinterpret_cast<float4*>(p) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
+          else
+            for (int e = 0; e < 4; ++e)
+              if (n + e < a.N) p[e] = v[k][e];
+        } else {
+          T* p = static_cast<T*>(a.y) + at;
+          if (vec) *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[k][0], v[k][1]), pack2<T>(v[k][2], v[k][3]));
+          else
+            for (int e = 0; e < 4; ++e)
+              if (n + e < a.N) p[e] = from_f32<T>(v[k][e]);
+        }
+      }
     }
   }
-  __syncwarp();
-  cluster_sync_all();  // no CTA leaves while another reads its partial tile
 }
 
 template <int BN, typename T, bool GATHER>
@@ -730,27 +809,40 @@ static cudaError_t launch_tc(const LinearArgs& a, int num_sms, cudaStream_t st) 
   const int dt = a.fp16 ? DIT_DTYPE_FP16 : DIT_DTYPE_BF16;
   const int kblocks = (a.K + 63) / 64;
   CUtensorMap tx, tw;
-  const long long tiles256 = static_cast<long long>((a.M + 255) / 256) * ((a.N + 255) / 256);
-  const long long tiles128 = static_cast<long long>((a.M + 255) / 256) * ((a.N + 127) / 128);
-  if (tiles128 >= num_sms / 2 && map_rows(&tx, dt, a.x, a.M, a.K, a.ldx, 128, 64)) {
-    const bool wide = !a.out_f32 && tiles256 >= num_sms / 2;
-    if (map_rows(&tw, dt, a.w, a.N, a.K, a.ldw, wide ? 128 : 64, 64)) {
-      if (a.out_f32) return launch_pair<128, T, true>(a, tx, tw, num_sms, st);
-      return wide ? launch_pair<256, T, false>(a, tx, tw, num_sms, st) : launch_pair<128, T, false>(a, tx, tw, num_sms, st);
-    }
+  // Tile width: a 64-wide K stage costs a pair 512 cycles at 256 columns (tensor cores) and about
+  // 440 at 192 (shared memory: 28 KB in, 28 KB out at 128 bytes a cycle), so the narrower tile
+  // pays where it leaves fewer or fuller rounds (N = 1152 at 8192 rows: 3 rounds of either).
+  const long long mt2 = (a.M + 255) / 256, pairs = num_sms / 2;
+  auto rounds = [&](int bn) { return (mt2 * ((a.N + bn - 1) / bn) + pairs - 1) / pairs; };
+  const int bn2 = rounds(192) * 440 < rounds(256) * 512 ? 192 : 256;
+  if (mt2 * ((a.N + 191) / 192) >= pairs && map_rows(&tx, dt, a.x, a.M, a.K, a.ldx, 128, 64) &&
+      map_rows(&tw, dt, a.w, a.N, a.K, a.ldw, bn2 / 2, 64)) {
+    if (a.out_f32) return bn2 == 192 ? launch_pair<192, T, true>(a, tx, tw, num_sms, st) : launch_pair<256, T, true>(a, tx, tw, num_sms, st);
+    return bn2 == 192 ? launch_pair<192, T, false>(a, tx, tw, num_sms, st) : launch_pair<256, T, false>(a, tx, tw, num_sms, st);
   }
   // the split kernel
   auto grain = [](const void* p, long long ld) {
     const uintptr_t v = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * 2);
     return v % 8 == 0 ? 8 : v % 4 == 0 ? 4 : 2;
   };
+  // Tile width and slices: each CTA copies in its stages at about 55 bytes a cycle, rounds of CTAs
+  // follow each other, and a round costs about 5000 cycles besides (set-up, first load, exchange).
   SplitArgs sp;
   const long long mt = (a.M + 127) / 128;
-  const bool narrow = mt * ((a.N + 127) / 128) < num_sms;
+  const int rows = a.M >= 128 ? 128 : a.M;
+  bool narrow = false;
+  long long best = -1;
+  for (int bn = 128; bn >= 64; bn -= 64)
+    for (int split = 1; split <= 8 && 2 * split <= kblocks + 1; split *= 2) {
+      const long long rounds = (mt * ((a.N + bn - 1) / bn) * split + num_sms - 1) / num_sms;
+      const long long cost = rounds * (5000 + (kblocks + split - 1) / split * ((rows + bn) * 128ll / 55));
+      if (best < 0 || cost < best) {
+        best = cost;
+        sp.split = split;
+        narrow = bn == 64;
+      }
+    }
   const int bn = narrow ? 64 : 128;
-  const long long tiles = mt * ((a.N + bn - 1) / bn);
-  sp.split = 1;
-  while (sp.split < 8 && tiles * sp.split * 2 <= 2 * num_sms && kblocks >= 4 * sp.split) sp.split *= 2;
   const int box_rows = a.M >= 128 ? 128 : (a.M + 7) / 8 * 8;
   sp.grain_x = map_rows(&tx, dt, a.x, a.M, a.K, a.ldx, box_rows, 64) ? 0 : grain(a.x, a.ldx);
   sp.grain_w = map_rows(&tw, dt, a.w, a.N, a.K, a.ldw, bn, 64) ? 0 : grain(a.w, a.ldw);
