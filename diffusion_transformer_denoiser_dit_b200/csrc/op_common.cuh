@@ -41,6 +41,11 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// v, which every lane holds, marked as one value for the warp (the compiler then keeps what depends
+// on it, branches among it, in uniform registers).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int warp_index() { return static_cast<int>(uniform(threadIdx.x >> 5)); }
+
 // One lane of a converged warp, the same each time.  The roles that issue TMA copies and MMAs
 // run their loops with the whole warp and elect a lane around the instructions alone: their
 // operands then stay warp-uniform.  With the loop inside `if (lane == 0)` the four MMAs and the
@@ -56,7 +61,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 // mbar_wait by a whole warp: false for every lane when it ran out for any
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+  return uniform(__all_sync(0xffffffffu, mbar_wait(bar, parity, status))) != 0;
 }
 
 }  // namespace dit

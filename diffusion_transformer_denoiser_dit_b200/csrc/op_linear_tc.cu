@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(384, 1)
   auto RES = [&](int w, int b) { return bar0 + 8u * (2 * C::STAGES + 4 + 2 * w + b); };
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::STAGES * C::STAGE + C::STAGING + 8 * (2 * C::STAGES + 20));
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const bool leader = rank == 0;
   const int cid = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(384, 1)
   __syncwarp();
   cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
-  const uint32_t tmem_base = *holder;
+  const uint32_t tmem_base = uniform(*holder);
   pdl_trigger();
   pdl_wait();
 
@@ -465,7 +465,7 @@ struct SplitCfg {
   // release) took 1.6 us measured, so 96 KB of stages fed an SM 31 bytes a cycle and no more.
   static constexpr int STAGES = (232448 - 1024 - 256 - PART) / STAGE;
   static constexpr int SMEM = 1024 + STAGES * STAGE + PART + 256;
-  static constexpr int TMEM = 2 * BN;                // two accumulators (chunks of a float32 sum)
+  static constexpr int TMEM = 4 * BN;                // up to four accumulators: chunks of a float32 sum
   // 16-byte unit u of partial row r: rows 8 apart in one bank group, neighbours in others
   static __device__ __forceinline__ uint32_t part_at(int r, int u) {
     return static_cast<uint32_t>(r) * (BN * 4) + static_cast<uint32_t>((u & ~7) | ((u ^ r) & 7)) * 16;
@@ -507,8 +507,8 @@ __device__ __forceinline__ void gather_tile(uint8_t* dst, const T* p, long long 
   }
 }
 
-__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float x, float y, float z, float w) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 struct SplitArgs {
@@ -527,11 +527,9 @@ __global__ void __launch_bounds__(192)
   const uint32_t sbase = smem_u32(smem), part = sbase + C::STAGES * C::STAGE, bar0 = part + C::PART;
   auto FULL = [&](int s) { return bar0 + 8u * s; };
   auto EMPTY = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
-  auto TFULL = [&](int i) { return bar0 + 8u * (2 * C::STAGES + i); };
-  auto TEMPTY = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 2 + i); };
-  const uint32_t drain = bar0 + 8u * (2 * C::STAGES + 4);
-  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::STAGES * C::STAGE + C::PART + 8 * (2 * C::STAGES + 5));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t done = bar0 + 8u * (2 * C::STAGES);  // the last product of this CTA is complete
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::STAGES * C::STAGE + C::PART + 8 * (2 * C::STAGES + 1));
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int m_tiles = (a.M + 127) / 128;
   const int tile = blockIdx.x / sp.split;
@@ -539,7 +537,9 @@ __global__ void __launch_bounds__(192)
   const int kblocks_all = (a.K + 63) / 64;
   const int kb_begin = static_cast<int>(static_cast<long long>(kblocks_all) * rank / sp.split);
   const int kb_end = static_cast<int>(static_cast<long long>(kblocks_all) * (rank + 1) / sp.split);
-  const int chunk = a.out_f32 ? kF32ChunkBlocks : kblocks_all;
+  // blocks per accumulator: all of them, or 512 products (a quarter of the slice if that is more)
+  const int nkb = kb_end - kb_begin;
+  const int chunk = a.out_f32 ? max(kF32ChunkBlocks, (nkb + 3) / 4) : nkb;
   // rows of the tile that one CTA of the cluster finishes
   const int share = (min(128, a.M - m0) + sp.split - 1) / sp.split;
   const int gathered = GATHER ? (sp.grain_x != 0) + (sp.grain_w != 0) : 0;
@@ -549,11 +549,7 @@ __global__ void __launch_bounds__(192)
       mbar_init(FULL(s), (gathered < 2 ? 1 : 0) + (gathered > 0 ? 128 : 0));
       mbar_init(EMPTY(s), 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(TFULL(i), 1);
-      mbar_init(TEMPTY(i), 128);
-    }
-    mbar_init(drain, 1);
+    mbar_init(done, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -563,7 +559,7 @@ __global__ void __launch_bounds__(192)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *holder;
+  const uint32_t tmem_base = uniform(*holder);
   pdl_trigger();
   pdl_wait();
 
@@ -597,101 +593,80 @@ __global__ void __launch_bounds__(192)
           if (armed & (1u << j)) mbar_wait_warp(FULL(j), j < s ? ph : ph ^ 1u, a.status);
     }
   } else if (warp == 1) {
-    {  // ---------------- MMA issuer
-      constexpr uint32_t idesc = idesc_16<T>(128, BN);
-      int s = 0, it = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int kb0 = kb_begin; kb0 < kb_end && ok; kb0 += chunk, ++it) {
-        if (!mbar_wait_warp(TEMPTY(it & 1), ((it >> 1) & 1) ^ 1u, a.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const int kb1 = min(kb0 + chunk, kb_end);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_warp(FULL(s), ph, a.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES;
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16_ss(tmem_base + (it & 1) * BN, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sb + k * 32), idesc,
-                          kb > kb0 || k > 0 ? 1u : 0u);
-            mma_commit(EMPTY(s));
-          }
-          __syncwarp();
-          if (++s == C::STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-        if (ok && elect_one()) mma_commit(TFULL(it & 1));
-        __syncwarp();
-      }
-      if (!ok) {  // the MMAs that were issued finish before TMEM is freed
-        if (elect_one()) mma_commit(drain);
-        __syncwarp();
-        mbar_wait(drain, 0, a.status);
-      }
-    }
-  } else {  // ------------------------ warps 2..5: gather, then the sums of one row per thread
-    const int tid = threadIdx.x - 64, q = warp & 3, r = q * 32 + lane;
-    bool ok = true;
-    int s = 0, it = 0;
-    uint32_t ph = 0;
-    float acc[BN];
-#pragma unroll
-    for (int i = 0; i < BN; ++i) acc[i] = 0.f;
-    for (int kb0 = kb_begin; kb0 < kb_end && ok; kb0 += chunk, ++it) {
-      if (GATHER && gathered > 0) {
-        const int kb1 = min(kb0 + chunk, kb_end);
-        for (int kb = kb0; kb < kb1 && ok; ++kb) {
-          ok = mbar_wait(EMPTY(s), ph ^ 1u, a.status);
-          if (!ok) break;
-          uint8_t* sa = smem + s * C::STAGE;
-          if (sp.grain_x)
-            gather_tile(sa, static_cast<const T*>(a.x), a.ldx, m0, a.M, kb * 64, a.K, 128, sp.grain_x, tid);
-          if (sp.grain_w)
-            gather_tile(sa + C::A_BYTES, static_cast<const T*>(a.w), a.ldw, n0, a.N, kb * 64, a.K, BN, sp.grain_w, tid);
-          fence_proxy_async_smem();
-          mbar_arrive(FULL(s));
-          if (++s == C::STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-      }
-      if (ok) ok = mbar_wait(TFULL(it & 1), (it >> 1) & 1, a.status);
-      __syncwarp();
-      if (__any_sync(0xffffffffu, !ok)) {
-        ok = false;
-        break;
-      }
+    // ---------------- MMA issuer
+    constexpr uint32_t idesc = idesc_16<T>(128, BN);
+    int s = 0, left = chunk;
+    uint32_t ph = 0, acc = tmem_base, fresh = 0;
+    for (int kb = 0; kb < nkb; ++kb) {
+      if (!mbar_wait_warp(FULL(s), ph, a.status)) break;
       tc_fence_after();
+      const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES;
+      if (elect_one()) {
 #pragma unroll
-      for (int c = 0; c < BN; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (it & 1) * BN + c, v);
-        tmem_ld_wait<32>(v);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc[c + i] += __uint_as_float(v[i]);
+        for (int k = 0; k < 4; ++k)
+          mma_bf16_ss(acc, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sb + k * 32), idesc, k > 0 ? 1u : fresh);
+        mma_commit(EMPTY(s));
       }
-      tc_fence_before();
-      mbar_arrive(TEMPTY(it & 1));
+      __syncwarp();
+      fresh = 1;
+      if (--left == 0) {
+        left = chunk;
+        acc += BN;
+        fresh = 0;
+      }
+      if (++s == C::STAGES) {
+        s = 0;
+        ph ^= 1u;
+      }
     }
-    // row r goes to the CTA that finishes it: CTA r / share keeps rows share * CTA .. of the tile,
-    // slice after slice
-    if (ok && m0 + r < a.M) {
-      const int owner = r / share;
-      const uint32_t base = mapa_shared(part, owner);
-      const int pr = rank * share + (r - owner * share);
+    // also after a wait that ran out: what was issued finishes before TMEM is freed
+    if (elect_one()) mma_commit(done);
+    __syncwarp();
+    mbar_wait_warp(done, 0, a.status);
+  } else {  // ------------------------ warps 2..5: gather, then one row of sums per thread
+    const int tid = threadIdx.x - 64, q = warp & 3, r = q * 32 + lane;
+    if (GATHER && gathered > 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int kb = kb_begin; kb < kb_end; ++kb) {
+        if (!mbar_wait(EMPTY(s), ph ^ 1u, a.status)) break;
+        uint8_t* sa = smem + s * C::STAGE;
+        if (sp.grain_x) gather_tile(sa, static_cast<const T*>(a.x), a.ldx, m0, a.M, kb * 64, a.K, 128, sp.grain_x, tid);
+        if (sp.grain_w)
+          gather_tile(sa + C::A_BYTES, static_cast<const T*>(a.w), a.ldw, n0, a.N, kb * 64, a.K, BN, sp.grain_w, tid);
+        fence_proxy_async_smem();
+        mbar_arrive(FULL(s));
+        if (++s == C::STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      __syncwarp();
+    }
+    // Row r goes to the CTA that finishes it: CTA r / share keeps rows share * CTA .. of the tile,
+    // slice after slice.  A short loop: code that runs once per launch costs its fetch.
+    if (m0 + q * 32 < a.M && mbar_wait_warp(done, 0, a.status)) {
+      tc_fence_after();
+      const int owner = r / share, pr = rank * share + (r - owner * share);
+      const uint32_t base = mapa_shared(part, min(owner, sp.split - 1)), t = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      const bool mine = m0 + r < a.M;
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(t + c, v);
+        tmem_ld_wait<16>(v);
+#pragma unroll 1
+        for (int j = chunk; j < nkb; j += chunk) {
+          uint32_t w[16];
+          tmem_ld16(t + (j / chunk) * BN + c, w);
+          tmem_ld_wait<16>(w);
 #pragma unroll
-      for (int u = 0; u < BN / 4; ++u)
-        st_cluster_f4(base + C::part_at(pr, u), acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+        }
+        if (mine)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_cluster_v4(base + C::part_at(pr, c / 4 + i), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
     }
   }
   __syncwarp();
@@ -702,74 +677,63 @@ __global__ void __launch_bounds__(192)
     tmem_dealloc(tmem_base, C::TMEM);
   }
   // this CTA's rows: a thread keeps its four columns and steps through the rows, slices added in
-  // their order; four rows at a time, so that the loads of a batch are in flight together
+  // their order
   constexpr int UNITS = BN / 4, STEP = 192 / UNITS;
   static_assert(192 % UNITS == 0, "whole rows per step");
   const int u = threadIdx.x % UNITS, n = n0 + 4 * u, r0 = m0 + rank * share, rows = min(share, a.M - r0);
-  if (n < a.N) {
-    float bias[4] = {};
-    add_bias<4>(a, n, bias);
-    const bool vec = sp.vec && n + 4 <= a.N;
-    for (int r = threadIdx.x / UNITS; r < rows; r += 4 * STEP) {
-      float v[4][4], res[4][4];
+  if (n >= a.N) return;
+  const bool vec = sp.vec && n + 4 <= a.N;
+  const int cols = min(4, a.N - n);
+#pragma unroll 1
+  for (int r = threadIdx.x / UNITS; r < rows; r += STEP) {
+    float v[4], res[4] = {};
+    const long long ar = (r0 + r) * a.ldr + n, ay = (r0 + r) * a.ldy + n;
+    if (a.residual) {
+      if (a.out_f32) {
+        const float* p = static_cast<const float*>(a.residual) + ar;
+        if (vec) *reinterpret_cast<float4*>(res) = *reinterpret_cast<const float4*>(p);
+        else
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int rr = r + k * STEP;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[k][e] = bias[e];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) res[k][e] = 0.f;
-        if (rr < rows && a.residual) {
-          const long long at = (r0 + rr) * a.ldr + n;
-          if (a.out_f32) {
-            const float* p = static_cast<const float*>(a.residual) + at;
-            if (vec) *reinterpret_cast<float4*>(res[k]) = *reinterpret_cast<const float4*>(p);
-            else
-              for (int e = 0; e < 4; ++e) res[k][e] = n + e < a.N ? p[e] : 0.f;
-          } else {
-            const T* p = static_cast<const T*>(a.residual) + at;
-            if (vec) {
-              const uint2 w = *reinterpret_cast<const uint2*>(p);
-              const float2 y0 = unpack2<T>(w.x), y1 = unpack2<T>(w.y);
-              res[k][0] = y0.x, res[k][1] = y0.y, res[k][2] = y1.x, res[k][3] = y1.y;
-            } else {
-              for (int e = 0; e < 4; ++e) res[k][e] = n + e < a.N ? to_f32(p[e]) : 0.f;
-            }
-          }
-        }
-      }
-      for (int j = 0; j < sp.split; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (r + k * STEP >= rows) break;
-          const uint4 p = ld_shared_v4(part + C::part_at(j * share + r + k * STEP, u));
-          v[k][0] += __uint_as_float(p.x), v[k][1] += __uint_as_float(p.y);
-          v[k][2] += __uint_as_float(p.z), v[k][3] += __uint_as_float(p.w);
-        }
-      with_act(a.act, [&](auto act) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[k][e] = activate<decltype(act)::value>(v[k][e]) + res[k][e];
-      });
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (r + k * STEP >= rows) break;
-        const long long at = (r0 + r + k * STEP) * a.ldy + n;
-        if (a.out_f32) {
-          float* p = static_cast<float*>(a.y) + at;
-          if (vec) *reinterpret_cast<float4*>(p) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
-          else
-            for (int e = 0; e < 4; ++e)
-              if (n + e < a.N) p[e] = v[k][e];
+          for (int e = 0; e < 4; ++e) res[e] = e < cols ? p[e] : 0.f;
+      } else {
+        const T* p = static_cast<const T*>(a.residual) + ar;
+        if (vec) {
+          const uint2 w = *reinterpret_cast<const uint2*>(p);
+          const float2 y0 = unpack2<T>(w.x), y1 = unpack2<T>(w.y);
+          res[0] = y0.x, res[1] = y0.y, res[2] = y1.x, res[3] = y1.y;
         } else {
-          T* p = static_cast<T*>(a.y) + at;
-          if (vec) *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[k][0], v[k][1]), pack2<T>(v[k][2], v[k][3]));
-          else
-            for (int e = 0; e < 4; ++e)
-              if (n + e < a.N) p[e] = from_f32<T>(v[k][e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) res[e] = e < cols ? to_f32(p[e]) : 0.f;
         }
       }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = a.bias && e < cols ? __ldg(a.bias + n + e) : 0.f;
+    for (int j = 0; j < sp.split; ++j) {
+      const uint4 p = ld_shared_v4(part + C::part_at(j * share + r, u));
+      v[0] += __uint_as_float(p.x), v[1] += __uint_as_float(p.y);
+      v[2] += __uint_as_float(p.z), v[3] += __uint_as_float(p.w);
+    }
+    with_act(a.act, [&](auto act) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = activate<decltype(act)::value>(v[e]);
+    });
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += res[e];
+    if (a.out_f32) {
+      float* p = static_cast<float*>(a.y) + ay;
+      if (vec) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < cols) p[e] = v[e];
+    } else {
+      T* p = static_cast<T*>(a.y) + ay;
+      if (vec) *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < cols) p[e] = from_f32<T>(v[e]);
     }
   }
 }
@@ -804,18 +768,49 @@ static cudaError_t launch_split(const LinearArgs& a, const CUtensorMap& tx, cons
   return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a, sp, box_rows);
 }
 
+// clusters of 1, 2, 4 and 8 CTAs of the split kernel that the device runs at one time
+template <typename T>
+static bool split_clusters(int* fit) {
+  static int of[kMaxDevices][4] = {};
+  const int dev = current_device();
+  if (dev < 0) return false;
+  if (of[dev][3] == 0) {
+    auto kernel = linear_split_kernel<64, T, false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SplitCfg<64>::SMEM) != cudaSuccess) return false;
+    for (int i = 0; i < 4; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(8 * 148);
+      cfg.blockDim = dim3(192);
+      cfg.dynamicSmemBytes = SplitCfg<64>::SMEM;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim = {1u << i, 1, 1};
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&of[dev][i], kernel, &cfg) != cudaSuccess || of[dev][i] <= 0) {
+        of[dev][3] = 0;
+        return false;
+      }
+    }
+  }
+  for (int i = 0; i < 4; ++i) fit[i] = of[dev][i];
+  return true;
+}
+
 template <typename T>
 static cudaError_t launch_tc(const LinearArgs& a, int num_sms, cudaStream_t st) {
   const int dt = a.fp16 ? DIT_DTYPE_FP16 : DIT_DTYPE_BF16;
   const int kblocks = (a.K + 63) / 64;
   CUtensorMap tx, tw;
-  // Tile width: a 64-wide K stage costs a pair 512 cycles at 256 columns (tensor cores) and about
-  // 440 at 192 (shared memory: 28 KB in, 28 KB out at 128 bytes a cycle), so the narrower tile
-  // pays where it leaves fewer or fuller rounds (N = 1152 at 8192 rows: 3 rounds of either).
+  // Tile width: a 64-wide K stage costs a pair 512 cycles at 256 columns (tensor cores) and
+  // about 400 at 192, so the narrower tile pays where it leaves fewer or fuller rounds
+  // (N = 1152 at 8192 rows: 3 rounds of either).
   const long long mt2 = (a.M + 255) / 256, pairs = num_sms / 2;
   auto rounds = [&](int bn) { return (mt2 * ((a.N + bn - 1) / bn) + pairs - 1) / pairs; };
-  const int bn2 = rounds(192) * 440 < rounds(256) * 512 ? 192 : 256;
-  if (mt2 * ((a.N + 191) / 192) >= pairs && map_rows(&tx, dt, a.x, a.M, a.K, a.ldx, 128, 64) &&
+  const int bn2 = rounds(192) * 400 < rounds(256) * 512 ? 192 : 256;
+  // fewer tiles than half the pairs: the split kernel (1024 x 1152 -> 4608, 72 of 74 pairs busy: 12.9
+  // against 24.6 us; 512 x 768 -> 2304, 24 busy: 8.5 against 8.0)
+  if (mt2 * ((a.N + 191) / 192) >= pairs / 2 && map_rows(&tx, dt, a.x, a.M, a.K, a.ldx, 128, 64) &&
       map_rows(&tw, dt, a.w, a.N, a.K, a.ldw, bn2 / 2, 64)) {
     if (a.out_f32) return bn2 == 192 ? launch_pair<192, T, true>(a, tx, tw, num_sms, st) : launch_pair<256, T, true>(a, tx, tw, num_sms, st);
     return bn2 == 192 ? launch_pair<192, T, false>(a, tx, tw, num_sms, st) : launch_pair<256, T, false>(a, tx, tw, num_sms, st);
@@ -825,17 +820,20 @@ static cudaError_t launch_tc(const LinearArgs& a, int num_sms, cudaStream_t st) 
     const uintptr_t v = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * 2);
     return v % 8 == 0 ? 8 : v % 4 == 0 ? 4 : 2;
   };
-  // Tile width and slices: each CTA copies in its stages at about 55 bytes a cycle, rounds of CTAs
-  // follow each other, and a round costs about 5000 cycles besides (set-up, first load, exchange).
+  // Tile width and slices, from what was measured in cycles: a K block is 370 whatever the tile (the
+  // issue of its four MMAs), a round of CTAs 5300 besides and 3600 / 7600 more to finish 128 rows of
+  // 64 / 128 columns.  A round is what fits at one time: clusters of 4 and 8 do not reach every SM.
   SplitArgs sp;
   const long long mt = (a.M + 127) / 128;
   const int rows = a.M >= 128 ? 128 : a.M;
+  int fit[4];
+  if (!split_clusters<T>(fit)) return cudaErrorInvalidConfiguration;
   bool narrow = false;
   long long best = -1;
   for (int bn = 128; bn >= 64; bn -= 64)
-    for (int split = 1; split <= 8 && 2 * split <= kblocks + 1; split *= 2) {
-      const long long rounds = (mt * ((a.N + bn - 1) / bn) * split + num_sms - 1) / num_sms;
-      const long long cost = rounds * (5000 + (kblocks + split - 1) / split * ((rows + bn) * 128ll / 55));
+    for (int i = 0, split = 1; i < 4 && 2 * split <= kblocks + 1; ++i, split *= 2) {
+      const long long rounds = (mt * ((a.N + bn - 1) / bn) + fit[i] - 1) / fit[i];
+      const long long cost = rounds * (5300 + (kblocks + split - 1) / split * 370 + (bn == 64 ? 3600 : 7600) * rows / 128);
       if (best < 0 || cost < best) {
         best = cost;
         sp.split = split;
