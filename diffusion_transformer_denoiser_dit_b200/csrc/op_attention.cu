@@ -1,5 +1,30 @@
-// Attention over packed sequences, grouped heads, causal or full.
+// Attention over packed sequences on the tensor cores: o_i = sum_j softmax_j(scale q_i . k_j) v_j.
+//
+// A query tile is 128 rows: TQ = 128 / G tokens of one sequence times the G heads that share a
+// key head, so K and V are read once per key head and one new token with G heads is one tile.
+// Two softmax warpgroups each own a query tile and one thread per row:
+//   S = Q K^T (128 x 128 keys) into TMEM, the row in registers, running maximum and sum in base 2
+//   (float32), probabilities as 16-bit back into TMEM, O += P V with P read from there.
+// O is rescaled only when the maximum grew by more than 2^8 (then in place, by its own threads),
+// so P <= 2^8 before the final division.  V is used as it lies (keys x features: the MN-major B
+// operand of the MMA).
+//
+// Pair form: an item is two neighbouring query tiles of one key head; both read the same K / V
+//   tiles from one ring.
+// Split form (single tokens, or too few tiles to fill the GPU): an item is one query tile; the
+//   CTAs of a cluster take consecutive parts of its keys, the two groups of a CTA every other
+//   key tile, from a ring each.  Partial (max, sum, O) rows are sent to the CTA that finishes the
+//   row over distributed shared memory and joined there in a fixed order.
+//
+// Roles: warp 0 TMA loads; warps 1, 2 issue the MMAs of group 0, 1; warp 3 finds the items
+// (sequence, tile, head) from the offsets in device memory, 32 sequences at a time, and hands
+// them to the others; warps 4-7, 8-11 softmax.  Rows outside the item's sequence are read by
+// TMA as they come: query rows are independent and not stored, scores of such keys are masked,
+// and their V rows are set to zero in shared memory, since 0 * NaN is NaN.
+// Every wait is bounded; no TMA multicast.
 #include <math.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "op_common.cuh"
@@ -7,61 +32,706 @@
 
 namespace dit {
 
-// One warp per (query token, head): a running maximum and sum over the keys, the dh features
-// spread over the lanes.
-template <typename T>
-__global__ void __launch_bounds__(128) attention_rows_kernel(const PackedAttnArgs a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * 4 + warp;
-  pdl_trigger();
-  pdl_wait();
-  if (item >= static_cast<long long>(a.total_q) * a.H) return;
-  const int tok = static_cast<int>(item / a.H), h = static_cast<int>(item % a.H);
-  int lo = 0, hi = a.n_seq;  // the last sequence that starts at or before tok
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.cu_q[mid] <= tok) lo = mid;
-    else hi = mid;
-  }
-  const int q0 = a.cu_q[lo], q1 = min(a.cu_q[lo + 1], a.total_q);
-  if (tok < q0 || tok >= q1) return;
-  const int k0 = min(max(a.cu_k[lo], 0), a.total_k), k1 = min(max(a.cu_k[lo + 1], k0), a.total_k);
-  const int nk = k1 - k0;
-  const int last = a.causal ? min(nk, tok - q0 + nk - (q1 - q0) + 1) : nk;
-  const T* q = static_cast<const T*>(a.q) + tok * a.q_tok + h * a.q_head;
-  const T* k = static_cast<const T*>(a.k) + k0 * a.k_tok + (h / (a.H / a.Hk)) * a.k_head;
-  const T* v = static_cast<const T*>(a.v) + k0 * a.v_tok + (h / (a.H / a.Hk)) * a.v_head;
-  float qf[4] = {}, o[4] = {};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < a.dh) qf[i] = to_f32(q[lane + 32 * i]) * a.scale;
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < last; ++j) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < a.dh) s = fmaf(qf[i], to_f32(k[j * a.k_tok + lane + 32 * i]), s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), c = expf(m - mn), p = expf(s - mn);
-    l = l * c + p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < a.dh) o[i] = fmaf(p, to_f32(v[j * a.v_tok + lane + 32 * i]), o[i] * c);
-    m = mn;
-  }
-  const float inv = last > 0 ? 1.f / l : 0.f;
-  T* out = static_cast<T*>(a.o) + tok * a.o_tok + h * a.o_head;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < a.dh) out[lane + 32 * i] = from_f32<T>(o[i] * inv);
-  if (lane == 0 && a.lse) a.lse[static_cast<long long>(h) * a.total_q + tok] = last > 0 ? m + logf(l) : -INFINITY;
+// One pair of probabilities in every kPolyEvery is exponentiated by a polynomial on the FMA pipe
+// (ex2_poly_f2, 7.5e-5 relative): the MUFU unit gives 16 exponentials a cycle and SM, as long for
+// a 128 x 128 tile as its two products at dh = 128.
+constexpr int kPolyEvery = 4;
+
+template <int NA, bool SPLIT>
+struct FaCfg {
+  static constexpr bool ALIAS = NA == 2;             // P takes the place of S in TMEM (O needs the rest)
+  static constexpr int ATOM = 128 * 128;             // 128 rows x 64 features
+  static constexpr int TILE = NA * ATOM;
+  static constexpr int QT = SPLIT ? 1 : 2;           // query tiles per item
+  static constexpr int QB = NA == 1 ? 2 : 1;         // Q buffers
+  static constexpr int Q_BYTES = QB * QT * TILE;
+  static constexpr int SLOTS = (224 * 1024 - Q_BYTES) / TILE;  // K / V tiles in flight, all rings
+  static constexpr int RINGS = SPLIT ? 2 : 1;
+  static constexpr int RS = SLOTS / RINGS;           // slots per ring
+  static constexpr int OFF_KV = Q_BYTES;
+  static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
+  static constexpr int SMEM = 1024 + OFF_BAR + 768;
+  static constexpr int THREADS = 384, REG_CTRL = 96, REG_SOFTMAX = 200;
+  static constexpr int REG_POOL = 128 * REG_CTRL + 256 * REG_SOFTMAX;
+  static_assert(SMEM <= 232448 && RS >= 3, "shared memory");
+};
+
+struct FaItem {
+  int tok0, ntok;   // first query token, query tokens (<= QT * TQ); ntok < 0: no more items
+  int k0, nk;       // first key token, keys of the sequence
+  int off;          // query token i of the item sees keys j <= off + i (causal)
+  int hk;           // key head
+  int t0, t1;       // pair: key tiles of group 0, 1; split: this CTA's key tiles t0 .. t1 - 1
+};
+
+template <int NA, bool SPLIT>
+struct FaBars {
+  using C = FaCfg<NA, SPLIT>;
+  enum { IF = 0, IE = 2, QF = 4, QE = 6, SF = 8, SR = 10, PF = 12, OD = 16, OF = 18, KF = 20, KE = KF + C::SLOTS, N = KE + C::SLOTS };
+  static_assert(8 * N + 16 + 2 * sizeof(FaItem) <= 768, "barrier area");
+};
+
+// V tile in shared memory, rows of keys, 64 features (128 bytes) per atom: MN-major, 128-byte
+// swizzle; 8-key groups 1024 bytes apart (stride), the next 64 features one atom on (leading)
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((128 * 128) >> 4) << 16) | (64ull << 32) |
+         (1ull << 46) | (2ull << 61);
 }
 
-cudaError_t launch_attention_packed(const PackedAttnArgs& a, int, cudaStream_t st) {
-  const long long blocks = (static_cast<long long>(a.total_q) * a.H + 3) / 4;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  if (a.fp16) return launch_kernel(attention_rows_kernel<__half>, dim3(blocks), dim3(128), 0, st, a);
-  return launch_kernel(attention_rows_kernel<__nv_bfloat16>, dim3(blocks), dim3(128), 0, st, a);
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+
+struct FaArgs {
+  PackedAttnArgs a;
+  int G, TQ;        // heads per key head, query tokens per tile
+  int split;        // CTAs per cluster (split form)
+  float sc;         // scale * log2(e)
+};
+
+template <int NA, typename T, bool SPLIT>
+__global__ void __launch_bounds__(384, 1)
+    attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FaArgs f) {
+  using C = FaCfg<NA, SPLIT>;
+  using B = FaBars<NA, SPLIT>;
+  const PackedAttnArgs& a = f.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem), bar0 = sbase + C::OFF_BAR;
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+  volatile FaItem* items = reinterpret_cast<volatile FaItem*>(smem + C::OFF_BAR + 8 * B::N);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * B::N + 2 * sizeof(FaItem));
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B::IF + i), 1);
+      mbar_init(bar(B::IE + i), 11);              // one arrival per warp that reads items
+      mbar_init(bar(B::QF + i), 1);
+      mbar_init(bar(B::QE + i), 2);               // both MMA warps
+      mbar_init(bar(B::SF + i), 1);
+      mbar_init(bar(B::SR + i), 4);               // the group's warps have S in registers
+      mbar_init(bar(B::PF + 2 * i), 4);           // P of keys 0-63, 64-127
+      mbar_init(bar(B::PF + 2 * i + 1), 4);
+      mbar_init(bar(B::OD + i), 1);
+      mbar_init(bar(B::OF + i), 4);
+    }
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(bar(B::KF + i), 1);
+      mbar_init(bar(B::KE + i), SPLIT ? 1 : 2);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = uniform(*holder);
+  pdl_trigger();
+  pdl_wait();
+
+  // the item of use n, read by a whole warp, its ring entry released at once
+  auto next_item = [&](int n, FaItem& it) -> bool {
+    const bool ok = mbar_wait_warp(bar(B::IF + (n & 1)), (n >> 1) & 1, a.status);
+    const volatile FaItem& s = items[n & 1];
+    it.tok0 = uniform(s.tok0), it.ntok = uniform(s.ntok), it.k0 = uniform(s.k0), it.nk = uniform(s.nk);
+    it.off = uniform(s.off), it.hk = uniform(s.hk), it.t0 = uniform(s.t0), it.t1 = uniform(s.t1);
+    __syncwarp();
+    if (elect_one()) mbar_arrive(bar(B::IE + (n & 1)));
+    __syncwarp();
+    return ok && it.ntok >= 0;
+  };
+  // A wait that ran out: the role does no more work, but keeps step in the exchanges; what it
+  // issued (copies, products: microseconds) is given a millisecond to end before the block leaves.
+  auto after_timeout = [&]() {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000u) {
+    }
+    __syncwarp();
+  };
+  // split form: partial rows are exchanged through the K / V slots once every CTA is done with them
+  auto exchange_others = [&]() {
+    if constexpr (SPLIT) {
+      __syncwarp();
+      cluster_sync_all();
+      cluster_sync_all();
+      named_barrier_sync(1, C::THREADS);
+    }
+  };
+
+  if (warp < 4) {
+    regs_dec<C::REG_CTRL>();
+    FaItem it;
+    if (warp == 0) {  // ---------------- loads
+      int slot[C::RINGS] = {};
+      uint32_t ph[C::RINGS] = {};
+      const uint32_t q_bytes = static_cast<uint32_t>(f.G * f.TQ) * 128;
+      bool ok = true;
+      for (int n = 0; next_item(n, it); ++n) {
+        const int qb = n % C::QB;
+        ok = ok && mbar_wait_warp(bar(B::QE + qb), ((n / C::QB) & 1) ^ 1, a.status);
+        const int ng = !SPLIT && it.ntok > f.TQ ? 2 : 1;
+        if (ok && elect_one()) {
+          mbar_arrive_expect_tx(bar(B::QF + qb), ng * NA * q_bytes);
+          for (int g = 0; g < ng; ++g)
+            for (int c = 0; c < NA; ++c)
+              tma_load_3d(sbase + (qb * C::QT + g) * C::TILE + c * C::ATOM, &tmQ, bar(B::QF + qb), c * 64, it.hk * f.G,
+                          it.tok0 + g * f.TQ);
+        }
+        __syncwarp();
+        const int j0 = SPLIT ? it.t0 : 0, j1 = SPLIT ? it.t1 : max(it.t0, it.t1);
+        for (int j = j0; j < j1 && ok; ++j) {
+          const int r = SPLIT ? (j - j0) & 1 : 0;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            int& s = slot[C::RINGS == 2 ? r : 0];
+            uint32_t& p = ph[C::RINGS == 2 ? r : 0];
+            const int at = r * C::RS + s;
+            if (!mbar_wait_warp(bar(B::KE + at), p ^ 1u, a.status)) {
+              ok = false;
+              break;
+            }
+            if (elect_one()) {
+              mbar_arrive_expect_tx(bar(B::KF + at), C::TILE);
+              for (int c = 0; c < NA; ++c)
+                tma_load_3d(sbase + C::OFF_KV + at * C::TILE + c * C::ATOM, kv ? &tmV : &tmK, bar(B::KF + at), c * 64, it.hk,
+                            it.k0 + j * 128);
+            }
+            __syncwarp();
+            if (++s == C::RS) {
+              s = 0;
+              p ^= 1u;
+            }
+          }
+        }
+        exchange_others();
+      }
+      if (!ok) after_timeout();
+    } else if (warp == 3) {  // ---------------- items
+      const int per = C::QT * f.TQ;                       // query tokens per item
+      const long long step = SPLIT ? gridDim.x / f.split : gridDim.x;
+      long long id = SPLIT ? blockIdx.x / f.split : blockIdx.x;
+      int sb = -32;                                        // sequences sb + lane are in registers
+      long long cum = 0;                                   // items (per head) before them
+      int q0 = 0, lq = 0, k0 = 0, lk = 0, tiles = 0, incl = 0, total = 0;
+      for (int n = 0;; ++n, id += step) {
+        const long long t = id / a.Hk;
+        while (sb < a.n_seq && t >= cum + total) {
+          cum += total;
+          sb += 32;
+          const int s = sb + lane;
+          q0 = lq = k0 = lk = tiles = 0;
+          if (s < a.n_seq) {  // offsets beyond the totals are cut: nothing outside the tensors is used
+            q0 = min(max(a.cu_q[s], 0), a.total_q);
+            lq = min(max(a.cu_q[s + 1], q0), a.total_q) - q0;
+            k0 = min(max(a.cu_k[s], 0), a.total_k);
+            lk = min(max(a.cu_k[s + 1], k0), a.total_k) - k0;
+            tiles = (lq + per - 1) / per;
+          }
+          incl = tiles;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+          }
+          total = __shfl_sync(0xffffffffu, incl, 31);
+        }
+        FaItem e{};
+        e.ntok = -1;
+        if (sb < a.n_seq) {
+          const int left = static_cast<int>(t - cum);
+          const int src = __ffs(__ballot_sync(0xffffffffu, incl > left)) - 1;
+          int tile = left - (__shfl_sync(0xffffffffu, incl, src) - __shfl_sync(0xffffffffu, tiles, src));
+          if (a.causal) tile = __shfl_sync(0xffffffffu, tiles, src) - 1 - tile;  // the longest first
+          const int Lq = __shfl_sync(0xffffffffu, lq, src), Lk = __shfl_sync(0xffffffffu, lk, src);
+          e.tok0 = __shfl_sync(0xffffffffu, q0, src) + tile * per;
+          e.ntok = min(per, Lq - tile * per);
+          e.k0 = __shfl_sync(0xffffffffu, k0, src);
+          e.nk = Lk;
+          e.off = tile * per + Lk - Lq;
+          e.hk = static_cast<int>(id - t * a.Hk);
+          // key tiles that query tokens up to the item's last-th see
+          auto seen = [&](int last) {
+            const int keys = a.causal ? min(Lk, e.off + last + 1) : Lk;
+            return keys > 0 ? (keys + 127) / 128 : 0;
+          };
+          if constexpr (SPLIT) {
+            const long long nt = seen(e.ntok - 1);
+            e.t0 = static_cast<int>(nt * rank / f.split);
+            e.t1 = static_cast<int>(nt * (rank + 1) / f.split);
+          } else {
+            e.t0 = seen(min(e.ntok, f.TQ) - 1);
+            e.t1 = e.ntok > f.TQ ? seen(e.ntok - 1) : 0;
+          }
+        }
+        if (!mbar_wait_warp(bar(B::IE + (n & 1)), ((n >> 1) & 1) ^ 1, a.status)) break;
+        if (elect_one()) {
+          volatile FaItem& s = items[n & 1];
+          s.tok0 = e.tok0, s.ntok = e.ntok, s.k0 = e.k0, s.nk = e.nk, s.off = e.off, s.hk = e.hk, s.t0 = e.t0, s.t1 = e.t1;
+          mbar_arrive(bar(B::IF + (n & 1)));
+        }
+        __syncwarp();
+        if (e.ntok < 0) break;
+        exchange_others();
+      }
+    } else {  // ---------------- MMA issue, group g
+      const int g = warp - 1;
+      constexpr uint32_t idesc_s = idesc_16<T>(128, 128);
+      const int n16 = (a.dh + 15) / 16;
+      const uint32_t idesc_o = idesc_16<T>(128, 16 * n16) | (1u << 16);  // B (V) is MN-major
+      const uint32_t tS = tmem_base + g * 128, tO = tmem_base + 256 + g * (NA == 1 ? 64 : 128);
+      const uint32_t tP = C::ALIAS ? tS : tmem_base + 384 + g * 64;
+      int ns = 0, np = 0, ni = 0;  // QK and PV issued; items with tiles
+      bool ok = true;
+      // K and V alternate in the ring: K of tile j + 1 lies two slots behind K of tile j, V of tile j between
+      int kslot = 0, vslot = 1;
+      uint32_t kph = 0, vph = 0;
+      auto step2 = [&](int& s, uint32_t& p) {
+        s += 2;
+        if (s >= C::RS) {
+          s -= C::RS;
+          p ^= 1u;
+        }
+      };
+      for (int n = 0; next_item(n, it); ++n) {
+        const int qb = n % C::QB;
+        int mine, all;  // key tiles of this group, of the ring
+        if constexpr (SPLIT) all = mine = (it.t1 - it.t0 + 1 - g) >> 1;
+        else {
+          mine = g == 0 ? it.t0 : it.t1;
+          all = max(it.t0, it.t1);
+        }
+        ok = ok && mbar_wait_warp(bar(B::QF + qb), (n / C::QB) & 1, a.status);
+        if (ok && mine == 0) {
+          if (elect_one()) mbar_arrive(bar(B::QE + qb));
+          __syncwarp();
+        }
+        const uint32_t qs = sbase + (qb * C::QT + (SPLIT ? 0 : g)) * C::TILE;
+        auto issue_qk = [&](int j) {
+          const int at = (SPLIT ? g * C::RS : 0) + kslot;
+          if (!mbar_wait_warp(bar(B::KF + at), kph, a.status)) {
+            ok = false;
+            return;
+          }
+          if (j < mine) {
+            // without aliasing S is free once the softmax has the previous one in registers; with it,
+            // the product that reads P in its place was issued before this one
+            if (!C::ALIAS && ns > 0 && !mbar_wait_warp(bar(B::SR + g), (ns - 1) & 1, a.status)) {
+              ok = false;
+              return;
+            }
+            tc_fence_after();
+            const uint32_t ks = sbase + C::OFF_KV + at * C::TILE;
+            if (elect_one()) {
+              for (int k = 0; k < n16; ++k) {
+                const uint32_t o = (k >> 2) * C::ATOM + (k & 3) * 32;
+                mma_bf16_ss(tS, sdesc_k_sw128(qs + o), sdesc_k_sw128(ks + o), idesc_s, k > 0 ? 1u : 0u);
+              }
+              mma_commit(bar(B::SF + g));
+              mma_commit(bar(B::KE + at));
+              if (j == mine - 1) mma_commit(bar(B::QE + qb));
+            }
+            ++ns;
+          } else if (elect_one()) {
+            mbar_arrive(bar(B::KE + at));
+          }
+          __syncwarp();
+          step2(kslot, kph);
+        };
+        auto issue_pv = [&](int j) {
+          const int at = (SPLIT ? g * C::RS : 0) + vslot;
+          if (!mbar_wait_warp(bar(B::KF + at), vph, a.status)) {
+            ok = false;
+            return;
+          }
+          if (j < mine) {
+            const uint32_t vs = sbase + C::OFF_KV + at * C::TILE;
+            const int valid = it.nk - (SPLIT ? it.t0 + 2 * j + g : j) * 128;
+            const int steps = min(8, (valid + 15) >> 4);
+            if (valid < 128 && (valid & 15)) {
+              // keys behind the sequence inside the last 16: their V rows become zero
+              const int rows = 16 - (valid & 15);
+              for (int i = lane; i < rows * 8 * NA; i += 32) {
+                const int c = i / (rows * 8), r = valid + (i >> 3) % rows;
+                *reinterpret_cast<uint4*>(smem + C::OFF_KV + at * C::TILE + c * C::ATOM + r * 128 + (i & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            // O of the previous item has been read
+            if (j == 0 && ni > 0 && !mbar_wait_warp(bar(B::OF + g), (ni - 1) & 1, a.status)) {
+              ok = false;
+              return;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!mbar_wait_warp(bar(B::PF + 2 * g + h), np & 1, a.status)) {
+                ok = false;
+                return;
+              }
+              tc_fence_after();
+              if (elect_one()) {
+                for (int k = 4 * h; k < min(4 * h + 4, steps); ++k)
+                  mma_bf16_ts(tO, tP + 8 * k, sdesc_mn_sw128(vs + k * 2048), idesc_o, j > 0 || k > 0 ? 1u : 0u);
+                if (h == 1) {
+                  mma_commit(bar(B::OD + g));
+                  mma_commit(bar(B::KE + at));
+                }
+              }
+              __syncwarp();
+            }
+            ++np;
+          } else if (elect_one()) {
+            mbar_arrive(bar(B::KE + at));
+          }
+          __syncwarp();
+          step2(vslot, vph);
+        };
+        if (ok && all > 0) issue_qk(0);
+        for (int j = 0; j < all && ok; ++j) {
+          if (!C::ALIAS && j + 1 < all) issue_qk(j + 1);
+          if (ok) issue_pv(j);
+          if (C::ALIAS && ok && j + 1 < all) issue_qk(j + 1);
+        }
+        if (mine > 0) ++ni;
+        exchange_others();
+      }
+      if (!ok) after_timeout();
+    }
+  } else {  // ---------------- softmax: group g, one query row per thread
+    regs_inc<C::REG_SOFTMAX>();
+    const int g = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    const uint32_t tS = tmem_base + lane_off + g * 128, tO = tmem_base + lane_off + 256 + g * (NA == 1 ? 64 : 128);
+    const uint32_t tP = C::ALIAS ? tS : tmem_base + lane_off + 384 + g * 64;
+    const int rt = r / f.G, rh = r - rt * f.G;  // token and head of this row within the tile
+    int cnt = 0;  // key tiles of this group so far
+    bool ok = true;
+    FaItem it;
+    for (int n = 0; next_item(n, it); ++n) {
+      const int tok = (SPLIT ? 0 : g * f.TQ) + rt;          // of the item
+      const bool row_ok = r < f.TQ * f.G && tok < it.ntok;
+      const bool warp_ok = __any_sync(0xffffffffu, row_ok); // else this warp only keeps step
+      const int lim = !row_ok ? 0 : a.causal ? min(it.nk, it.off + tok + 1) : it.nk;  // keys this row sees
+      const int mine = SPLIT ? (it.t1 - it.t0 + 1 - g) >> 1 : g == 0 ? it.t0 : it.t1;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < mine && ok; ++j, ++cnt) {
+        const int key0 = (SPLIT ? it.t0 + 2 * j + g : j) * 128;
+        if (!mbar_wait_warp(bar(B::SF + g), cnt & 1, a.status)) {
+          ok = false;
+          break;
+        }
+        if (!warp_ok) {
+          if (!C::ALIAS) {
+            if (elect_one()) mbar_arrive(bar(B::SR + g));
+            // this S may be there before the previous P is: no warp arrives for two tiles at once
+            if (j > 0 && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) {
+              ok = false;
+              break;
+            }
+          }
+          __syncwarp();
+          if (elect_one()) {
+            mbar_arrive(bar(B::PF + 2 * g));
+            mbar_arrive(bar(B::PF + 2 * g + 1));
+          }
+          __syncwarp();
+          continue;
+        }
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s + c * 32);
+        tmem_ld_wait<128>(s);
+        if (!C::ALIAS) {
+          tc_fence_before();
+          __syncwarp();
+          if (elect_one()) mbar_arrive(bar(B::SR + g));
+          __syncwarp();
+        }
+        const int nvalid = lim - key0;
+        if (__any_sync(0xffffffffu, nvalid < 128)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= nvalid) s[i] = __float_as_uint(-INFINITY);
+        }
+        float mp[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mp[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+#pragma unroll
+        for (int i = 8; i < 128; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mp[e] = max3f(mp[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
+        const float m_new = fmaxf(m_ref, fmaxf(max3f(mp[0], mp[1], mp[2]), mp[3]) * f.sc);
+        if (j == 0) {
+          m_ref = m_new;
+        } else if (__any_sync(0xffffffffu, m_new - m_ref > 8.0f)) {
+          // O moves to the new maximum.  Its last product is complete: with aliasing it came before this S in
+          // the same pipe, otherwise its barrier says so.
+          const float alpha = m_ref == m_new ? 1.0f : ex2_approx(m_ref - m_new);
+          m_ref = m_new;
+          if (!C::ALIAS && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < a.dh; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(tO + c, o);
+            tmem_ld_wait<16>(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st16(tO + c, o);
+          }
+          tmem_st_wait();
+          l *= alpha;
+        }
+        // P's place is free once the previous product has read it (with aliasing: it has)
+        if (!C::ALIAS && cnt > 0 && j > 0 && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) {
+          ok = false;
+          break;
+        }
+        const float mu = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen no key yet
+        const uint64_t sc2 = f2_pack(f.sc, f.sc), nm2 = f2_pack(-mu, -mu);
+        uint64_t rs2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int e = 64 * h + 2 * i;
+            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, nm2);
+            uint64_t p2;
+            if (i % kPolyEvery == kPolyEvery - 1) {
+              p2 = ex2_poly_f2(x2);
+            } else {
+              float x0, x1;
+              f2_unpack(x2, x0, x1);
+              p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
+            }
+            rs2[i & 1] = f2_add(rs2[i & 1], p2);
+            float p0, p1;
+            f2_unpack(p2, p0, p1);
+            pk[i] = pack2<T>(p0, p1);
+          }
+          tmem_st32(tP + 32 * h, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (elect_one()) mbar_arrive(bar(B::PF + 2 * g + h));
+          __syncwarp();
+        }
+        float r0, r1, r2, r3;
+        f2_unpack(rs2[0], r0, r1);
+        f2_unpack(rs2[1], r2, r3);
+        l += (r0 + r1) + (r2 + r3);
+      }
+      ok = ok && (mine == 0 || mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status));
+      if (!SPLIT && !ok) break;
+      tc_fence_after();
+      const int head = it.hk * f.G + rh;
+      if constexpr (!SPLIT) {
+        if (warp_ok) {
+          const float inv = lim > 0 ? 1.0f / l : 0.f;
+          T* out = static_cast<T*>(a.o) + (it.tok0 + tok) * a.o_tok + head * a.o_head;
+#pragma unroll 1
+          for (int c = 0; c < a.dh; c += 16) {
+            uint32_t o[16];
+            if (mine > 0) {
+              tmem_ld16(tO + c, o);
+              tmem_ld_wait<16>(o);
+            }
+            if (row_ok) {
+              uint32_t p[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                p[i] = lim > 0 ? pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
+              *reinterpret_cast<uint4*>(out + c) = make_uint4(p[0], p[1], p[2], p[3]);
+              if (c + 8 < a.dh) *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+            }
+          }
+          if (row_ok && a.lse)
+            a.lse[static_cast<long long>(head) * a.total_q + it.tok0 + tok] =
+                lim > 0 ? (m_ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (mine > 0 && elect_one()) mbar_arrive(bar(B::OF + g));
+        __syncwarp();
+      } else {
+        // Rows go to the CTA that finishes them: CTA r / share keeps rows share * CTA ..; the partial
+        // of CTA c, group g is slot 2 c + g: O rows [slot][row][16 n16] float32, then (max, sum) [slot][row].
+        cluster_sync_all();
+        const int rows = min(f.TQ, it.ntok) * f.G, share = (rows + f.split - 1) / f.split;
+        const int wide = (a.dh + 15) / 16 * 64;  // bytes of a row
+        const uint32_t part = sbase + C::OFF_KV, stats = part + 2 * f.split * share * wide;
+        if (q * 32 < rows) {
+          const int owner = min(r / share, f.split - 1), pr = (2 * rank + g) * share + r - owner * share;
+          const uint32_t peer = mapa_shared(part, owner) + pr * wide;
+#pragma unroll 1
+          for (int c = 0; c < a.dh && mine > 0; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(tO + c, o);
+            tmem_ld_wait<16>(o);
+            if (r < rows)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) st_cluster_v4(peer + c * 4 + i * 16, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+          if (r < rows) st_cluster_v2(mapa_shared(stats, owner) + pr * 8, m_ref, l);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (mine > 0 && elect_one()) mbar_arrive(bar(B::OF + g));
+        __syncwarp();
+        cluster_sync_all();
+        // eight columns of one row per thread and step
+        const int units = a.dh / 8, mrows = min(share, rows - rank * share);
+        const uint8_t* gp = smem + C::OFF_KV;
+        const float2* gs = reinterpret_cast<const float2*>(gp + 2 * f.split * share * wide);
+#pragma unroll 1
+        for (int i = threadIdx.x - 128; i < mrows * units; i += 256) {
+          const int lr = i / units, u = i - lr * units, row = rank * share + lr, t = row / f.G, hd = it.hk * f.G + row - t * f.G;
+          float mx = -INFINITY;
+          for (int p = 0; p < 2 * f.split; ++p) mx = fmaxf(mx, gs[p * share + lr].x);
+          float sum = 0.f, o[8] = {};
+          for (int p = 0; p < 2 * f.split; ++p) {
+            const float2 st = gs[p * share + lr];
+            if (st.x == -INFINITY) continue;  // nothing seen: its O row was not written
+            const float w = ex2_approx(st.x - mx);
+            sum += w * st.y;
+            const float4* src = reinterpret_cast<const float4*>(gp + (p * share + lr) * wide + u * 32);
+            const float4 x = src[0], y = src[1];
+            o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
+            o[4] += w * y.x, o[5] += w * y.y, o[6] += w * y.z, o[7] += w * y.w;
+          }
+          const bool any = mx != -INFINITY;
+          const float inv = any ? 1.0f / sum : 0.f;
+          T* out = static_cast<T*>(a.o) + (it.tok0 + t) * a.o_tok + hd * a.o_head + 8 * u;
+          *reinterpret_cast<uint4*>(out) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                                                      pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+          if (u == 0 && a.lse)
+            a.lse[static_cast<long long>(hd) * a.total_q + it.tok0 + t] = any ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        }
+        fence_proxy_async_smem();  // the slots are TMA's again
+        __syncwarp();
+        named_barrier_sync(1, C::THREADS);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (SPLIT) cluster_sync_all();  // no CTA leaves while another may write to it
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <int NA, typename T, bool SPLIT>
+static cudaError_t launch_fa(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FaArgs& f, int ctas,
+                             cudaStream_t st) {
+  using C = FaCfg<NA, SPLIT>;
+  auto kernel = attention_tc_kernel<NA, T, SPLIT>;
+  static bool set[kMaxDevices] = {};
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    // the register split (setmaxnreg) must fit in the launch allocation, or it would wait forever
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * C::THREADS < C::REG_POOL) return cudaErrorInvalidConfiguration;
+    set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (SPLIT) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n++].val.clusterDim = {static_cast<unsigned>(f.split), 1, 1};
+  }
+  if (g_pdl) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, f);
+}
+
+template <int NA, typename T>
+static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, FaArgs& f, int num_sms,
+                               cudaStream_t st) {
+  const PackedAttnArgs& a = f.a;
+  // most items there can be: every sequence ends inside a tile
+  auto items = [&](long long per) {
+    const long long by_len = (static_cast<long long>(a.max_q) + per - 1) / per * a.n_seq;
+    const long long by_total = a.total_q / per + a.n_seq;
+    return (by_len > 0 && by_len < by_total ? by_len : by_total) * a.Hk;
+  };
+  const long long pairs = items(2 * f.TQ), singles = items(f.TQ);
+  const int nt = (a.max_k + 127) / 128;
+  // One query tile per sequence, or fewer pairs than half the SMs: the split form
+  if (a.max_q > f.TQ && pairs * 2 > num_sms) {
+    return launch_fa<NA, T, false>(tq, tk, tv, f, static_cast<int>(pairs < num_sms ? pairs : num_sms), st);
+  }
+  f.split = 1;
+  while (f.split < 8 && singles * f.split * 2 <= num_sms && nt >= 4 * f.split) f.split *= 2;
+  const long long clusters = singles < num_sms / f.split ? singles : num_sms / f.split;
+  return launch_fa<NA, T, true>(tq, tk, tv, f, static_cast<int>(clusters) * f.split, st);
+}
+
+template <typename T>
+static cudaError_t launch_t(const PackedAttnArgs& a, int num_sms, cudaStream_t st) {
+  FaArgs f;
+  f.a = a;
+  f.G = a.H / a.Hk;
+  f.TQ = 128 / f.G;
+  f.split = 1;
+  f.sc = a.scale * 1.4426950408889634f;
+  const int dt = a.fp16 ? DIT_DTYPE_FP16 : DIT_DTYPE_BF16;
+  CUtensorMap tq, tk, tv;
+  auto map = [&](CUtensorMap* m, const void* p, long long heads, long long tokens, long long head, long long tok, int box_h,
+                 int box_t) {
+    // an axis of length 1 is never stepped along: any valid stride does
+    const uint64_t sh = heads > 1 ? 2 * head : 2 * a.dh, stk = tokens > 1 ? 2 * tok : 2 * a.dh;
+    const uint64_t dims[3] = {static_cast<uint64_t>(a.dh), static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens)};
+    const uint64_t strides[2] = {sh, stk};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(box_h), static_cast<uint32_t>(box_t)};
+    return make_tmap_view(m, dt, p, 3, dims, strides, box);
+  };
+  if (!map(&tq, a.q, a.H, a.total_q, a.q_head, a.q_tok, f.G, f.TQ)) return cudaErrorInvalidValue;
+  if (a.total_k == 0) {
+    tk = tv = tq;  // no key tile is ever loaded
+  } else if (!map(&tk, a.k, a.Hk, a.total_k, a.k_head, a.k_tok, 1, 128) ||
+             !map(&tv, a.v, a.Hk, a.total_k, a.v_head, a.v_tok, 1, 128)) {
+    return cudaErrorInvalidValue;
+  }
+  return a.dh <= 64 ? launch_form<1, T>(tq, tk, tv, f, num_sms, st) : launch_form<2, T>(tq, tk, tv, f, num_sms, st);
+}
+
+cudaError_t launch_attention_packed(const PackedAttnArgs& a, int num_sms, cudaStream_t st) {
+  return a.fp16 ? launch_t<__half>(a, num_sms, st) : launch_t<__nv_bfloat16>(a, num_sms, st);
 }
 
 }  // namespace dit

@@ -1,6 +1,8 @@
 // Element types of the packed-layer building blocks: loads to and stores from float32.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -62,6 +64,19 @@ __device__ __forceinline__ bool elect_one() {
 // mbar_wait by a whole warp: false for every lane when it ran out for any
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
   return uniform(__all_sync(0xffffffffu, mbar_wait(bar, parity, status))) != 0;
+}
+
+// Instruction descriptor, kind::f16: A and B both fp16 or both bf16, K-major, f32 accumulator.
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N) {
+  constexpr uint32_t f = std::is_same<T, __half>::value ? 0u : 1u;
+  return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// 16 bytes into the shared memory of a CTA of the cluster (address from mapa)
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 }  // namespace dit

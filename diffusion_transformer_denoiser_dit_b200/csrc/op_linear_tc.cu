@@ -32,14 +32,6 @@ namespace dit {
 
 constexpr int kF32ChunkBlocks = 8;  // 64-wide K blocks per accumulator when the output is float32
 
-// Instruction descriptor, kind::f16: A and B both fp16 or both bf16, K-major, f32 accumulator.
-template <typename T>
-__host__ __device__ constexpr uint32_t idesc_16(int M, int N) {
-  constexpr uint32_t f = std::is_same<T, __half>::value ? 0u : 1u;
-  return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
-}
-
 // v[i] += bias[n + i] for i < W; columns at or past N get nothing
 template <int W>
 __device__ __forceinline__ void add_bias(const LinearArgs& a, int n, float* v) {
@@ -507,9 +499,6 @@ __device__ __forceinline__ void gather_tile(uint8_t* dst, const T* p, long long 
   }
 }
 
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
 
 struct SplitArgs {
   int split;            // CTAs per cluster: K slices of a tile
