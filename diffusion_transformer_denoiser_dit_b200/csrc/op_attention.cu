@@ -2,9 +2,11 @@
 //
 // A query tile is 128 rows: TQ = 128 / G tokens of one sequence times the G heads that share a
 // key head, so K and V are read once per key head and one new token with G heads is one tile.
-// Two softmax warpgroups each own a query tile and one thread per row:
-//   S = Q K^T (128 x 128 keys) into TMEM, the row in registers, running maximum and sum in base 2
-//   (float32), probabilities as 16-bit back into TMEM, O += P V with P read from there.
+// Two softmax groups of eight warps each own a query tile:
+//   S = Q K^T (128 x 128 keys) into TMEM, half a row in each of two threads' registers, running
+//   maximum and sum in base 2 (float32), probabilities as 16-bit back into TMEM, O += P V with P
+//   read from there.  Two threads per row: with one, the two warps of a scheduler left it idle half
+//   the time (period of a tile pair at dh = 64: 3100 cycles for 1536 of exponentials).
 // O is rescaled only when the maximum grew by more than 2^8 (then in place, by its own threads),
 // so P <= 2^8 before the final division.  V is used as it lies (keys x features: the MN-major B
 // operand of the MMA).
@@ -16,9 +18,9 @@
 //   key tile, from a ring each.  Partial (max, sum, O) rows are sent to the CTA that finishes the
 //   row over distributed shared memory and joined there in a fixed order.
 //
-// Roles: warp 0 TMA loads; warps 1, 2 issue the MMAs of group 0, 1; warp 3 finds the items
+// Roles: warp 0 TMA loads; warp 1 issues the MMAs; warp 3 finds the items
 // (sequence, tile, head) from the offsets in device memory, 32 sequences at a time, and hands
-// them to the others; warps 4-7, 8-11 softmax.  Rows outside the item's sequence are read by
+// them to the others; warps 4-11, 12-19 softmax.  Rows outside the item's sequence are read by
 // TMA as they come: query rows are independent and not stored, scores of such keys are masked,
 // and their V rows are set to zero in shared memory, since 0 * NaN is NaN.
 // Every wait is bounded; no TMA multicast.
@@ -40,6 +42,7 @@ constexpr int kPolyEvery = 4;
 template <int NA, bool SPLIT>
 struct FaCfg {
   static constexpr bool ALIAS = NA == 2;             // P takes the place of S in TMEM (O needs the rest)
+  static constexpr int P1 = ALIAS ? 64 : 32;         // columns from P of keys 0-63 to P of keys 64-127
   static constexpr int ATOM = 128 * 128;             // 128 rows x 64 features
   static constexpr int TILE = NA * ATOM;
   static constexpr int QT = SPLIT ? 1 : 2;           // query tiles per item
@@ -50,9 +53,10 @@ struct FaCfg {
   static constexpr int RS = SLOTS / RINGS;           // slots per ring
   static constexpr int OFF_KV = Q_BYTES;
   static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
-  static constexpr int SMEM = 1024 + OFF_BAR + 768;
-  static constexpr int THREADS = 384, REG_CTRL = 96, REG_SOFTMAX = 200;
-  static constexpr int REG_POOL = 128 * REG_CTRL + 256 * REG_SOFTMAX;
+  static constexpr int OFF_ROW = OFF_BAR + 448;      // one float per query row: the halves' exchange
+  static constexpr int SMEM = 1024 + OFF_ROW + 1024;
+  static constexpr int THREADS = 640, REG_CTRL = 64, REG_SOFTMAX = 104;
+  static constexpr int REG_POOL = 128 * REG_CTRL + 512 * REG_SOFTMAX;
   static_assert(SMEM <= 232448 && RS >= 3, "shared memory");
 };
 
@@ -68,14 +72,14 @@ template <int NA, bool SPLIT>
 struct FaBars {
   using C = FaCfg<NA, SPLIT>;
   enum { IF = 0, IE = 2, QF = 4, QE = 6, SF = 8, SR = 10, PF = 12, OD = 16, OF = 18, KF = 20, KE = KF + C::SLOTS, N = KE + C::SLOTS };
-  static_assert(8 * N + 16 + 2 * sizeof(FaItem) <= 768, "barrier area");
+  static_assert(8 * N + 16 + 2 * sizeof(FaItem) <= 448, "barrier area");
 };
 
 // V tile in shared memory, rows of keys, 64 features (128 bytes) per atom: MN-major, 128-byte
 // swizzle; 8-key groups 1024 bytes apart (stride), the next 64 features one atom on (leading)
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((128 * 128) >> 4) << 16) | (64ull << 32) |
-         (1ull << 46) | (2ull << 61);
+// (the low word; the high word is kSdescHiSw128)
+__device__ __forceinline__ uint32_t sdesc_mn_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | (((128u * 128u) >> 4) << 16);
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
@@ -88,6 +92,20 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t addr, float x, float y) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 
+// whether v holds for any thread of the two warps that meet at barrier `id`
+__device__ __forceinline__ bool any_of_pair(uint32_t id, bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned p, %2, 64, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(v)), "r"(id)
+      : "memory");
+  return any != 0;
+}
+
 struct FaArgs {
   PackedAttnArgs a;
   int G, TQ;        // heads per key head, query tokens per tile
@@ -96,7 +114,7 @@ struct FaArgs {
 };
 
 template <int NA, typename T, bool SPLIT>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(640, 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FaArgs f) {
   using C = FaCfg<NA, SPLIT>;
@@ -114,19 +132,19 @@ __global__ void __launch_bounds__(384, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B::IF + i), 1);
-      mbar_init(bar(B::IE + i), 11);              // one arrival per warp that reads items
+      mbar_init(bar(B::IE + i), 19);              // one arrival per warp that reads items
       mbar_init(bar(B::QF + i), 1);
-      mbar_init(bar(B::QE + i), 2);               // both MMA warps
+      mbar_init(bar(B::QE + i), 1);
       mbar_init(bar(B::SF + i), 1);
-      mbar_init(bar(B::SR + i), 4);               // the group's warps have S in registers
+      mbar_init(bar(B::SR + i), 8);               // the group's warps have S in registers
       mbar_init(bar(B::PF + 2 * i), 4);           // P of keys 0-63, 64-127
       mbar_init(bar(B::PF + 2 * i + 1), 4);
       mbar_init(bar(B::OD + i), 1);
-      mbar_init(bar(B::OF + i), 4);
+      mbar_init(bar(B::OF + i), 8);
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(bar(B::KF + i), 1);
-      mbar_init(bar(B::KE + i), SPLIT ? 1 : 2);
+      mbar_init(bar(B::KE + i), 1);
     }
     fence_barrier_init();
   }
@@ -166,7 +184,7 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
       cluster_sync_all();
       cluster_sync_all();
-      named_barrier_sync(1, C::THREADS);
+      named_barrier_sync(9, C::THREADS);
     }
   };
 
@@ -285,18 +303,21 @@ __global__ void __launch_bounds__(384, 1)
         if (e.ntok < 0) break;
         exchange_others();
       }
-    } else {  // ---------------- MMA issue, group g
-      const int g = warp - 1;
+    } else if (warp == 1) {  // ---------------- MMA issue
+      // One warp issues for both groups in turn, O_g += P_g V_j and S_g = Q_g K_j+1 of one before those of
+      // the other, so that the groups work half a period apart: one's exponentials run beside the other's
+      // products.  (Issued by a warp per group, both groups' products finished together and the two took
+      // turns with the tensor cores as one: period 5000 cycles at dh = 128 for 2048 of products.)
       constexpr uint32_t idesc_s = idesc_16<T>(128, 128);
       const int n16 = (a.dh + 15) / 16;
       const uint32_t idesc_o = idesc_16<T>(128, 16 * n16) | (1u << 16);  // B (V) is MN-major
-      const uint32_t tS = tmem_base + g * 128, tO = tmem_base + 256 + g * (NA == 1 ? 64 : 128);
-      const uint32_t tP = C::ALIAS ? tS : tmem_base + 384 + g * 64;
-      int ns = 0, np = 0, ni = 0;  // QK and PV issued; items with tiles
+      int ns[2] = {}, np[2] = {}, ni[2] = {};  // per group: QK and PV issued; items with tiles
       bool ok = true;
-      // K and V alternate in the ring: K of tile j + 1 lies two slots behind K of tile j, V of tile j between
-      int kslot = 0, vslot = 1;
-      uint32_t kph = 0, vph = 0;
+      // K and V alternate in a ring: K of tile j + 1 lies two slots behind K of tile j, V of tile j between
+      int kslot[C::RINGS] = {}, vslot[C::RINGS];
+      uint32_t kph[C::RINGS] = {}, vph[C::RINGS] = {};
+#pragma unroll
+      for (int i = 0; i < C::RINGS; ++i) vslot[i] = 1;
       auto step2 = [&](int& s, uint32_t& p) {
         s += 2;
         if (s >= C::RS) {
@@ -304,119 +325,159 @@ __global__ void __launch_bounds__(384, 1)
           p ^= 1u;
         }
       };
+      auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && mbar_wait_warp(b, parity, a.status); };
       for (int n = 0; next_item(n, it); ++n) {
         const int qb = n % C::QB;
-        int mine, all;  // key tiles of this group, of the ring
-        if constexpr (SPLIT) all = mine = (it.t1 - it.t0 + 1 - g) >> 1;
-        else {
-          mine = g == 0 ? it.t0 : it.t1;
-          all = max(it.t0, it.t1);
+        int mine[2];  // key tiles of each group
+        if constexpr (SPLIT) {
+          mine[0] = (it.t1 - it.t0 + 1) >> 1;
+          mine[1] = (it.t1 - it.t0) >> 1;
+        } else {
+          mine[0] = it.t0;
+          mine[1] = it.t1;
         }
-        ok = ok && mbar_wait_warp(bar(B::QF + qb), (n / C::QB) & 1, a.status);
-        if (ok && mine == 0) {
-          if (elect_one()) mbar_arrive(bar(B::QE + qb));
-          __syncwarp();
-        }
-        const uint32_t qs = sbase + (qb * C::QT + (SPLIT ? 0 : g)) * C::TILE;
-        auto issue_qk = [&](int j) {
-          const int at = (SPLIT ? g * C::RS : 0) + kslot;
-          if (!mbar_wait_warp(bar(B::KF + at), kph, a.status)) {
-            ok = false;
-            return;
-          }
-          if (j < mine) {
-            // without aliasing S is free once the softmax has the previous one in registers; with it,
-            // the product that reads P in its place was issued before this one
-            if (!C::ALIAS && ns > 0 && !mbar_wait_warp(bar(B::SR + g), (ns - 1) & 1, a.status)) {
-              ok = false;
-              return;
-            }
-            tc_fence_after();
-            const uint32_t ks = sbase + C::OFF_KV + at * C::TILE;
-            if (elect_one()) {
-              for (int k = 0; k < n16; ++k) {
-                const uint32_t o = (k >> 2) * C::ATOM + (k & 3) * 32;
-                mma_bf16_ss(tS, sdesc_k_sw128(qs + o), sdesc_k_sw128(ks + o), idesc_s, k > 0 ? 1u : 0u);
-              }
-              mma_commit(bar(B::SF + g));
-              mma_commit(bar(B::KE + at));
-              if (j == mine - 1) mma_commit(bar(B::QE + qb));
-            }
-            ++ns;
-          } else if (elect_one()) {
-            mbar_arrive(bar(B::KE + at));
-          }
-          __syncwarp();
-          step2(kslot, kph);
-        };
-        auto issue_pv = [&](int j) {
-          const int at = (SPLIT ? g * C::RS : 0) + vslot;
-          if (!mbar_wait_warp(bar(B::KF + at), vph, a.status)) {
-            ok = false;
-            return;
-          }
-          if (j < mine) {
-            const uint32_t vs = sbase + C::OFF_KV + at * C::TILE;
-            const int valid = it.nk - (SPLIT ? it.t0 + 2 * j + g : j) * 128;
-            const int steps = min(8, (valid + 15) >> 4);
-            if (valid < 128 && (valid & 15)) {
-              // keys behind the sequence inside the last 16: their V rows become zero
-              const int rows = 16 - (valid & 15);
-              for (int i = lane; i < rows * 8 * NA; i += 32) {
-                const int c = i / (rows * 8), r = valid + (i >> 3) % rows;
-                *reinterpret_cast<uint4*>(smem + C::OFF_KV + at * C::TILE + c * C::ATOM + r * 128 + (i & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-            // O of the previous item has been read
-            if (j == 0 && ni > 0 && !mbar_wait_warp(bar(B::OF + g), (ni - 1) & 1, a.status)) {
-              ok = false;
-              return;
-            }
+        const int all = max(mine[0], mine[1]);
+        wait(bar(B::QF + qb), (n / C::QB) & 1);
+        // S_g = Q_g K_j from the slot `at`
+        auto issue_qk = [&](int g, int at) {
+          // without aliasing S is free once the softmax has the previous one in registers; with it,
+          // the product that reads P in its place was issued before this one
+          if (!C::ALIAS && ns[g] > 0) wait(bar(B::SR + g), (ns[g] - 1) & 1);
+          tc_fence_after();
+          const uint32_t qd = sdesc_lo(sbase + (qb * C::QT + (SPLIT ? 0 : g)) * C::TILE);
+          const uint32_t kd = sdesc_lo(sbase + C::OFF_KV + at * C::TILE), tS = tmem_base + g * 128;
+          if (ok && elect_one()) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!mbar_wait_warp(bar(B::PF + 2 * g + h), np & 1, a.status)) {
-                ok = false;
-                return;
-              }
-              tc_fence_after();
-              if (elect_one()) {
-                for (int k = 4 * h; k < min(4 * h + 4, steps); ++k)
-                  mma_bf16_ts(tO, tP + 8 * k, sdesc_mn_sw128(vs + k * 2048), idesc_o, j > 0 || k > 0 ? 1u : 0u);
-                if (h == 1) {
-                  mma_commit(bar(B::OD + g));
-                  mma_commit(bar(B::KE + at));
-                }
-              }
-              __syncwarp();
+            for (int k = 0; k < 4 * NA; ++k) {
+              const uint32_t o = ((k >> 2) * C::ATOM + (k & 3) * 32) >> 4;
+              if (k < n16)
+                mma_bf16_ss(tS, sdesc_make(qd + o, kSdescHiSw128), sdesc_make(kd + o, kSdescHiSw128), idesc_s, k > 0 ? 1u : 0u);
             }
-            ++np;
-          } else if (elect_one()) {
-            mbar_arrive(bar(B::KE + at));
+            mma_commit(bar(B::SF + g));
           }
           __syncwarp();
-          step2(vslot, vph);
+          ++ns[g];
         };
-        if (ok && all > 0) issue_qk(0);
-        for (int j = 0; j < all && ok; ++j) {
-          if (!C::ALIAS && j + 1 < all) issue_qk(j + 1);
-          if (ok) issue_pv(j);
-          if (C::ALIAS && ok && j + 1 < all) issue_qk(j + 1);
+        // O_g (+)= P_g V_j from the slot `at`, whose keys start at key0
+        auto issue_pv = [&](int g, int at, int j, int key0) {
+          // O of the previous item has been read
+          if (j == 0 && ni[g] > 0) wait(bar(B::OF + g), (ni[g] - 1) & 1);
+          const int steps = min(8, (it.nk - key0 + 15) >> 4);
+          const uint32_t vd = sdesc_mn_lo(sbase + C::OFF_KV + at * C::TILE);
+          const uint32_t tO = tmem_base + 256 + g * (NA == 1 ? 64 : 128);
+          const uint32_t tP = C::ALIAS ? tmem_base + g * 128 : tmem_base + 384 + g * 64;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            wait(bar(B::PF + 2 * g + h), np[g] & 1);
+            tc_fence_after();
+            if (ok && elect_one()) {
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)
+                if (k < steps)
+                  mma_bf16_ts(tO, tP + h * C::P1 + 8 * (k & 3), sdesc_make(vd + k * (2048 >> 4), kSdescHiSw128), idesc_o,
+                              j > 0 || k > 0 ? 1u : 0u);
+              if (h == 1) mma_commit(bar(B::OD + g));
+            }
+            __syncwarp();
+          }
+          ++np[g];
+        };
+        // keys behind the sequence inside the last 16 of a V tile: their rows become zero
+        auto clear_tail = [&](int at, int key0) {
+          const int valid = it.nk - key0;
+          if (valid >= 128 || (valid & 15) == 0) return;
+          const int rows = 16 - (valid & 15);
+          for (int i = lane; i < rows * 8 * NA; i += 32) {
+            const int c = i / (rows * 8), r = valid + (i >> 3) % rows;
+            *reinterpret_cast<uint4*>(smem + C::OFF_KV + at * C::TILE + c * C::ATOM + r * 128 + (i & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        };
+        auto release = [&](uint32_t b) {  // once the products issued so far are complete
+          if (elect_one()) mma_commit(b);
+          __syncwarp();
+        };
+        if constexpr (SPLIT) {
+          auto k_of = [&](int g) {
+            const int at = g * C::RS + kslot[g % C::RINGS];
+            wait(bar(B::KF + at), kph[g % C::RINGS]);
+            issue_qk(g, at);
+            release(bar(B::KE + at));
+            step2(kslot[g % C::RINGS], kph[g % C::RINGS]);
+          };
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            if (mine[g] > 0) k_of(g);
+          for (int j = 0; j < all; ++j) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              if (j >= mine[g]) continue;
+              if (!C::ALIAS && j + 1 < mine[g]) k_of(g);
+              const int at = g * C::RS + vslot[g % C::RINGS], key0 = (it.t0 + 2 * j + g) * 128;
+              wait(bar(B::KF + at), vph[g % C::RINGS]);
+              clear_tail(at, key0);
+              issue_pv(g, at, j, key0);
+              release(bar(B::KE + at));
+              step2(vslot[g % C::RINGS], vph[g % C::RINGS]);
+              if (C::ALIAS && j + 1 < mine[g]) k_of(g);
+            }
+          }
+        } else {
+          if (all > 0) {
+            wait(bar(B::KF + kslot[0]), kph[0]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+              if (mine[g] > 0) issue_qk(g, kslot[0]);
+            release(bar(B::KE + kslot[0]));
+            step2(kslot[0], kph[0]);
+          }
+          for (int j = 0; j < all; ++j) {
+            const int kat = kslot[0], vat = vslot[0];
+            if (j + 1 < all) wait(bar(B::KF + kat), kph[0]);
+            wait(bar(B::KF + vat), vph[0]);
+            clear_tail(vat, j * 128);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              if (!C::ALIAS && j + 1 < mine[g]) issue_qk(g, kat);
+              if (j < mine[g]) issue_pv(g, vat, j, j * 128);
+              if (C::ALIAS && j + 1 < mine[g]) issue_qk(g, kat);
+            }
+            release(bar(B::KE + vat));
+            step2(vslot[0], vph[0]);
+            if (j + 1 < all) {
+              release(bar(B::KE + kat));
+              step2(kslot[0], kph[0]);
+            }
+          }
         }
-        if (mine > 0) ++ni;
+        release(bar(B::QE + qb));
+#pragma unroll
+        for (int g = 0; g < 2; ++g) ni[g] += mine[g] > 0;
         exchange_others();
       }
       if (!ok) after_timeout();
+    } else {  // ---------------- warp 2 only keeps step
+      for (int n = 0; next_item(n, it); ++n) exchange_others();
     }
-  } else {  // ---------------- softmax: group g, one query row per thread
+  } else {  // ---------------- softmax: group g, two threads per query row, 64 keys of a tile each
     regs_inc<C::REG_SOFTMAX>();
-    const int g = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;
+    const int g = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, q = warp & 3, r = q * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
-    const uint32_t tS = tmem_base + lane_off + g * 128, tO = tmem_base + lane_off + 256 + g * (NA == 1 ? 64 : 128);
-    const uint32_t tP = C::ALIAS ? tS : tmem_base + lane_off + 384 + g * 64;
+    const uint32_t tS = tmem_base + lane_off + g * 128 + hf * 64, tO = tmem_base + lane_off + 256 + g * (NA == 1 ? 64 : 128);
+    const uint32_t tP = C::ALIAS ? tS : tmem_base + lane_off + 384 + g * 64 + hf * 32;
     const int rt = r / f.G, rh = r - rt * f.G;  // token and head of this row within the tile
+    const uint32_t pair = 1 + g * 4 + q;        // named barrier of the two warps that share 32 rows
+    volatile float* row = reinterpret_cast<volatile float*>(smem + C::OFF_ROW) + g * 128 + r;
+    // f(half 0's value, half 1's value) to both halves of a row
+    auto join = [&](float v, auto&& fn) {
+      if (hf == 1) *row = v;
+      named_barrier_sync(pair, 64);
+      if (hf == 0) *row = v = fn(v, *row);
+      named_barrier_sync(pair, 64);
+      return hf == 1 ? static_cast<float>(*row) : v;
+    };
     int cnt = 0;  // key tiles of this group so far
     bool ok = true;
     FaItem it;
@@ -428,33 +489,24 @@ __global__ void __launch_bounds__(384, 1)
       const int mine = SPLIT ? (it.t1 - it.t0 + 1 - g) >> 1 : g == 0 ? it.t0 : it.t1;
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < mine && ok; ++j, ++cnt) {
-        const int key0 = (SPLIT ? it.t0 + 2 * j + g : j) * 128;
-        if (!mbar_wait_warp(bar(B::SF + g), cnt & 1, a.status)) {
-          ok = false;
-          break;
-        }
+        const int key0 = (SPLIT ? it.t0 + 2 * j + g : j) * 128 + hf * 64;
+        if (!mbar_wait_warp(bar(B::SF + g), cnt & 1, a.status)) ok = false;
         if (!warp_ok) {
           if (!C::ALIAS) {
             if (elect_one()) mbar_arrive(bar(B::SR + g));
             // this S may be there before the previous P is: no warp arrives for two tiles at once
-            if (j > 0 && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) {
-              ok = false;
-              break;
-            }
+            if (ok && j > 0 && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) ok = false;
           }
           __syncwarp();
-          if (elect_one()) {
-            mbar_arrive(bar(B::PF + 2 * g));
-            mbar_arrive(bar(B::PF + 2 * g + 1));
-          }
+          if (elect_one()) mbar_arrive(bar(B::PF + 2 * g + hf));
           __syncwarp();
           continue;
         }
         tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s + c * 32);
-        tmem_ld_wait<128>(s);
+        uint32_t s[64];
+        tmem_ld32(tS, s);
+        tmem_ld32(tS + 32, s + 32);
+        tmem_ld_wait<64>(s);
         if (!C::ALIAS) {
           tc_fence_before();
           __syncwarp();
@@ -462,78 +514,76 @@ __global__ void __launch_bounds__(384, 1)
           __syncwarp();
         }
         const int nvalid = lim - key0;
-        if (__any_sync(0xffffffffu, nvalid < 128)) {
+        if (__any_sync(0xffffffffu, nvalid < 64)) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
+          for (int i = 0; i < 64; ++i)
             if (i >= nvalid) s[i] = __float_as_uint(-INFINITY);
         }
         float mp[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) mp[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
 #pragma unroll
-        for (int i = 8; i < 128; i += 8)
+        for (int i = 8; i < 64; i += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) mp[e] = max3f(mp[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
-        const float m_new = fmaxf(m_ref, fmaxf(max3f(mp[0], mp[1], mp[2]), mp[3]) * f.sc);
-        if (j == 0) {
-          m_ref = m_new;
-        } else if (__any_sync(0xffffffffu, m_new - m_ref > 8.0f)) {
-          // O moves to the new maximum.  Its last product is complete: with aliasing it came before this S in
-          // the same pipe, otherwise its barrier says so.
+        const float mx = fmaxf(max3f(mp[0], mp[1], mp[2]), mp[3]) * f.sc;
+        // The reference moves only when a row's maximum grew by more than 2^8 (or is the first): the two
+        // warps of the row agree on that by a barrier that also ors, and only then exchange their maxima
+        if (any_of_pair(pair, mx > m_ref + 8.0f)) {
+          const float m_new = fmaxf(m_ref, join(mx, [](float x, float y) { return fmaxf(x, y); }));
           const float alpha = m_ref == m_new ? 1.0f : ex2_approx(m_ref - m_new);
           m_ref = m_new;
-          if (!C::ALIAS && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < a.dh; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(tO + c, o);
-            tmem_ld_wait<16>(o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st16(tO + c, o);
-          }
-          tmem_st_wait();
           l *= alpha;
+          if (j > 0) {
+            // O moves to the new maximum, each half every other 16 columns.  Its last product is complete:
+            // with aliasing it came before this S in the same pipe, otherwise its barrier says so.
+            if (!C::ALIAS && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) ok = false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 16 * hf; c < a.dh; c += 32) {
+              uint32_t o[16];
+              tmem_ld16(tO + c, o);
+              tmem_ld_wait<16>(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(tO + c, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            named_barrier_sync(pair, 64);  // all of O before either half's P lets the next product start
+          }
         }
         // P's place is free once the previous product has read it (with aliasing: it has)
-        if (!C::ALIAS && cnt > 0 && j > 0 && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) {
-          ok = false;
-          break;
-        }
+        if (!C::ALIAS && j > 0 && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) ok = false;
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen no key yet
         const uint64_t sc2 = f2_pack(f.sc, f.sc), nm2 = f2_pack(-mu, -mu);
         uint64_t rs2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
+        uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int e = 64 * h + 2 * i;
-            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, nm2);
-            uint64_t p2;
-            if (i % kPolyEvery == kPolyEvery - 1) {
-              p2 = ex2_poly_f2(x2);
-            } else {
-              float x0, x1;
-              f2_unpack(x2, x0, x1);
-              p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
-            }
-            rs2[i & 1] = f2_add(rs2[i & 1], p2);
-            float p0, p1;
-            f2_unpack(p2, p0, p1);
-            pk[i] = pack2<T>(p0, p1);
+        for (int i = 16 * h; i < 16 * h + 16; ++i) {
+          const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, nm2);
+          uint64_t p2;
+          if (i % kPolyEvery == kPolyEvery - 1) {
+            p2 = ex2_poly_f2(x2);
+          } else {
+            float x0, x1;
+            f2_unpack(x2, x0, x1);
+            p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
           }
-          tmem_st32(tP + 32 * h, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (elect_one()) mbar_arrive(bar(B::PF + 2 * g + h));
-          __syncwarp();
+          rs2[i & 1] = f2_add(rs2[i & 1], p2);
+          float p0, p1;
+          f2_unpack(p2, p0, p1);
+          pk[i - 16 * h] = pack2<T>(p0, p1);
         }
+        tmem_st16(tP + 16 * h, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (elect_one()) mbar_arrive(bar(B::PF + 2 * g + hf));
+        __syncwarp();
         float r0, r1, r2, r3;
         f2_unpack(rs2[0], r0, r1);
         f2_unpack(rs2[1], r2, r3);
@@ -542,13 +592,14 @@ __global__ void __launch_bounds__(384, 1)
       ok = ok && (mine == 0 || mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status));
       if (!SPLIT && !ok) break;
       tc_fence_after();
+      if (warp_ok) l = join(l, [](float x, float y) { return x + y; });
       const int head = it.hk * f.G + rh;
       if constexpr (!SPLIT) {
         if (warp_ok) {
           const float inv = lim > 0 ? 1.0f / l : 0.f;
           T* out = static_cast<T*>(a.o) + (it.tok0 + tok) * a.o_tok + head * a.o_head;
 #pragma unroll 1
-          for (int c = 0; c < a.dh; c += 16) {
+          for (int c = 16 * hf; c < a.dh; c += 32) {
             uint32_t o[16];
             if (mine > 0) {
               tmem_ld16(tO + c, o);
@@ -563,7 +614,7 @@ __global__ void __launch_bounds__(384, 1)
               if (c + 8 < a.dh) *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(p[4], p[5], p[6], p[7]);
             }
           }
-          if (row_ok && a.lse)
+          if (row_ok && hf == 0 && a.lse)
             a.lse[static_cast<long long>(head) * a.total_q + it.tok0 + tok] =
                 lim > 0 ? (m_ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
@@ -582,7 +633,7 @@ __global__ void __launch_bounds__(384, 1)
           const int owner = min(r / share, f.split - 1), pr = (2 * rank + g) * share + r - owner * share;
           const uint32_t peer = mapa_shared(part, owner) + pr * wide;
 #pragma unroll 1
-          for (int c = 0; c < a.dh && mine > 0; c += 16) {
+          for (int c = 16 * hf; c < a.dh && mine > 0; c += 32) {
             uint32_t o[16];
             tmem_ld16(tO + c, o);
             tmem_ld_wait<16>(o);
@@ -590,7 +641,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) st_cluster_v4(peer + c * 4 + i * 16, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
-          if (r < rows) st_cluster_v2(mapa_shared(stats, owner) + pr * 8, m_ref, l);
+          if (r < rows && hf == 0) st_cluster_v2(mapa_shared(stats, owner) + pr * 8, m_ref, l);
         }
         tc_fence_before();
         __syncwarp();
@@ -602,7 +653,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint8_t* gp = smem + C::OFF_KV;
         const float2* gs = reinterpret_cast<const float2*>(gp + 2 * f.split * share * wide);
 #pragma unroll 1
-        for (int i = threadIdx.x - 128; i < mrows * units; i += 256) {
+        for (int i = threadIdx.x - 128; i < mrows * units; i += 512) {
           const int lr = i / units, u = i - lr * units, row = rank * share + lr, t = row / f.G, hd = it.hk * f.G + row - t * f.G;
           float mx = -INFINITY;
           for (int p = 0; p < 2 * f.split; ++p) mx = fmaxf(mx, gs[p * share + lr].x);
@@ -627,7 +678,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         fence_proxy_async_smem();  // the slots are TMA's again
         __syncwarp();
-        named_barrier_sync(1, C::THREADS);
+        named_barrier_sync(9, C::THREADS);
       }
     }
   }
