@@ -71,7 +71,7 @@ struct FaItem {
 template <int NA, bool SPLIT>
 struct FaBars {
   using C = FaCfg<NA, SPLIT>;
-  enum { IF = 0, IE = 2, QF = 4, QE = 6, SF = 8, SR = 10, PF = 12, OD = 16, OF = 18, KF = 20, KE = KF + C::SLOTS, N = KE + C::SLOTS };
+  enum { IF = 0, IE = 2, QF = 4, QE = 6, SF = 8, SR = 10, PF = 12, OD = 14, OF = 16, KF = 18, KE = KF + C::SLOTS, N = KE + C::SLOTS };
   static_assert(8 * N + 16 + 2 * sizeof(FaItem) <= 448, "barrier area");
 };
 
@@ -80,6 +80,23 @@ struct FaBars {
 // (the low word; the high word is kSdescHiSw128)
 __device__ __forceinline__ uint32_t sdesc_mn_lo(uint32_t saddr) {
   return ((saddr & 0x3FFFFu) >> 4) | (((128u * 128u) >> 4) << 16);
+}
+
+// S = Q K^T over STEPS x 16 features (operands in 64-feature atoms)
+template <int STEPS>
+__device__ __forceinline__ void mma_qk(uint32_t tS, uint32_t qd, uint32_t kd, uint32_t idesc) {
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    const uint32_t o = ((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4;
+    mma_bf16_ss(tS, sdesc_make(qd + o, kSdescHiSw128), sdesc_make(kd + o, kSdescHiSw128), idesc, k > 0 ? 1u : 0u);
+  }
+}
+// O (+)= P V over STEPS x 16 keys; P1 columns from P of the first 64 keys to the others
+template <int STEPS, int P1>
+__device__ __forceinline__ void mma_pv(uint32_t tO, uint32_t tP, uint32_t vd, uint32_t idesc, uint32_t more) {
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k)
+    mma_bf16_ts(tO, tP + (k >> 2) * P1 + 8 * (k & 3), sdesc_make(vd + k * (2048 >> 4), kSdescHiSw128), idesc, k > 0 ? 1u : more);
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
@@ -137,8 +154,7 @@ __global__ void __launch_bounds__(640, 1)
       mbar_init(bar(B::QE + i), 1);
       mbar_init(bar(B::SF + i), 1);
       mbar_init(bar(B::SR + i), 8);               // the group's warps have S in registers
-      mbar_init(bar(B::PF + 2 * i), 4);           // P of keys 0-63, 64-127
-      mbar_init(bar(B::PF + 2 * i + 1), 4);
+      mbar_init(bar(B::PF + i), 8);               // the group's warps have written P
       mbar_init(bar(B::OD + i), 1);
       mbar_init(bar(B::OF + i), 8);
     }
@@ -346,13 +362,14 @@ __global__ void __launch_bounds__(640, 1)
           tc_fence_after();
           const uint32_t qd = sdesc_lo(sbase + (qb * C::QT + (SPLIT ? 0 : g)) * C::TILE);
           const uint32_t kd = sdesc_lo(sbase + C::OFF_KV + at * C::TILE), tS = tmem_base + g * 128;
+          // 16 features a step; features past dh are zeros in shared memory, so the step count is one of few
+          // and the products are issued without a branch between them (about 40 cycles each; with a
+          // condition at each, 85, more than most of them run)
           if (ok && elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4 * NA; ++k) {
-              const uint32_t o = ((k >> 2) * C::ATOM + (k & 3) * 32) >> 4;
-              if (k < n16)
-                mma_bf16_ss(tS, sdesc_make(qd + o, kSdescHiSw128), sdesc_make(kd + o, kSdescHiSw128), idesc_s, k > 0 ? 1u : 0u);
-            }
+            if (NA == 1) mma_qk<4>(tS, qd, kd, idesc_s);
+            else if (n16 == 5) mma_qk<5>(tS, qd, kd, idesc_s);
+            else if (n16 == 6) mma_qk<6>(tS, qd, kd, idesc_s);
+            else mma_qk<8>(tS, qd, kd, idesc_s);
             mma_commit(bar(B::SF + g));
           }
           __syncwarp();
@@ -366,20 +383,20 @@ __global__ void __launch_bounds__(640, 1)
           const uint32_t vd = sdesc_mn_lo(sbase + C::OFF_KV + at * C::TILE);
           const uint32_t tO = tmem_base + 256 + g * (NA == 1 ? 64 : 128);
           const uint32_t tP = C::ALIAS ? tmem_base + g * 128 : tmem_base + 384 + g * 64;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            wait(bar(B::PF + 2 * g + h), np[g] & 1);
-            tc_fence_after();
-            if (ok && elect_one()) {
-#pragma unroll
-              for (int k = 4 * h; k < 4 * h + 4; ++k)
-                if (k < steps)
-                  mma_bf16_ts(tO, tP + h * C::P1 + 8 * (k & 3), sdesc_make(vd + k * (2048 >> 4), kSdescHiSw128), idesc_o,
-                              j > 0 || k > 0 ? 1u : 0u);
-              if (h == 1) mma_commit(bar(B::OD + g));
+          wait(bar(B::PF + g), np[g] & 1);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            const uint32_t more = j > 0 ? 1u : 0u;
+            if (steps == 8) {
+              mma_pv<8, C::P1>(tO, tP, vd, idesc_o, more);
+            } else {
+              mma_pv<1, C::P1>(tO, tP, vd, idesc_o, more);
+              for (int k = 1; k < steps; ++k)
+                mma_pv<1, C::P1>(tO, tP + (k >> 2) * C::P1 + 8 * (k & 3), vd + k * (2048 >> 4), idesc_o, 1u);
             }
-            __syncwarp();
+            mma_commit(bar(B::OD + g));
           }
+          __syncwarp();
           ++np[g];
         };
         // keys behind the sequence inside the last 16 of a V tile: their rows become zero
@@ -498,7 +515,7 @@ __global__ void __launch_bounds__(640, 1)
             if (ok && j > 0 && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) ok = false;
           }
           __syncwarp();
-          if (elect_one()) mbar_arrive(bar(B::PF + 2 * g + hf));
+          if (elect_one()) mbar_arrive(bar(B::PF + g));
           __syncwarp();
           continue;
         }
@@ -582,7 +599,7 @@ __global__ void __launch_bounds__(640, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (elect_one()) mbar_arrive(bar(B::PF + 2 * g + hf));
+        if (elect_one()) mbar_arrive(bar(B::PF + g));
         __syncwarp();
         float r0, r1, r2, r3;
         f2_unpack(rs2[0], r0, r1);

@@ -63,7 +63,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 // mbar_wait by a whole warp: false for every lane when it ran out for any
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
-  return uniform(__all_sync(0xffffffffu, mbar_wait(bar, parity, status))) != 0;
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
 // Instruction descriptor, kind::f16: A and B both fp16 or both bf16, K-major, f32 accumulator.
