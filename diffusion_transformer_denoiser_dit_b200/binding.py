@@ -321,24 +321,29 @@ def linear_e4m3(x8, w8, sx, sw, b, block_n: int = 128, stream=None):
 
 
 # ---------------------------------------------------------------- building blocks of packed layers
+# A call's own kernel may last three microseconds, so these look at each argument once and take
+# torch's raw stream and device handles instead of building Stream and device objects.
+
+_Strides8 = c_longlong * 8
+_RT = None
 
 
-def _codes():
-    import torch
-    return {torch.float32: DIT_DTYPE_F32, torch.bfloat16: DIT_DTYPE_BF16, torch.float16: DIT_DTYPE_FP16}
+class _Runtime:
+    def __init__(self):
+        import torch
+        self.torch, self.lib = torch, load()
+        self.float32, self.int32, self.int64 = torch.float32, torch.int32, torch.int64
+        self.code = {torch.float32: DIT_DTYPE_F32, torch.bfloat16: DIT_DTYPE_BF16, torch.float16: DIT_DTYPE_FP16}
+        self.code16 = {torch.bfloat16: DIT_DTYPE_BF16, torch.float16: DIT_DTYPE_FP16}
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent without CUDA
+        self.current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-_DTYPE_CODES = None
-
-
-def _dtype_code(dtype, floats32: bool, what: str) -> int:
-    global _DTYPE_CODES
-    if _DTYPE_CODES is None:
-        _DTYPE_CODES = _codes()
-    code = _DTYPE_CODES.get(dtype, -1)
-    if code < 0 or (code == DIT_DTYPE_F32 and not floats32):
-        raise TypeError(f"{what}: dtype {dtype} is not supported")
-    return code
+def _rt() -> _Runtime:
+    global _RT
+    if _RT is None:
+        _RT = _Runtime()
+    return _RT
 
 
 def _need(ok: bool, what: str):
@@ -346,39 +351,52 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _call(fn, name: str, tensors, stream, *args):
+def _no_dtype(name: str, dtype):
+    raise TypeError(f"{name}: dtype {dtype} is not supported")
+
+
+def _enqueue(rt: _Runtime, name: str, fn, tensors, stream, args):
     """fn(*args, stream) on the tensors' device and stream; raises DitError on a refusal."""
-    import torch
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors on {t.device} and {dev}")
-    if dev.type != "cuda":
+    dev = tensors[0].get_device()
+    if dev < 0:
         raise ValueError(f"{name}: needs CUDA tensors")
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _call(fn, name, tensors, stream, *args)
-    current = torch.cuda.current_stream()
-    if stream is None:
-        stream = current
-    elif stream != current:
-        if stream.device != dev:
-            raise ValueError(f"{name}: stream on {stream.device}, tensors on {dev}")
-        for t in tensors:  # their memory is not given away before the work on this stream is done
-            if t is not None:
-                t.record_stream(stream)
-    rc = fn(*args, stream.cuda_stream)
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: tensors on {t.device} and {tensors[0].device}")
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"{name}: stream on {stream.device}, tensors on {tensors[0].device}")
+        raw = stream.cuda_stream
+        if raw != rt.raw_stream(dev):
+            for t in tensors:  # their memory is not given away before the work on this stream is done
+                if t is not None:
+                    t.record_stream(stream)
+    else:
+        raw = rt.raw_stream(dev)
+    if dev != rt.current_device():
+        with rt.torch.cuda.device(dev):
+            rc = fn(*args, raw)
+    else:
+        rc = fn(*args, raw)
     if rc != DIT_OK:
         raise DitError(rc, f"{name}: {status_string(rc)}")
 
 
-def _fresh(shape, dtype, device, stream):
-    """An output on the stream that will write it."""
-    import torch
+def _fresh(like, shape, dtype, stream):
+    """An output on like's device, from the stream that will write it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
+    with _rt().torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _row_stride(t, name: str) -> int:
+    """Stride between the rows of a matrix whose rows are contiguous; that of a single row is free."""
+    rows, cols = t.shape
+    if t.is_contiguous():
+        return cols
+    _need(cols == 1 or t.stride(1) == 1, name + ": last strides must be 1")
+    return t.stride(0) if rows > 1 else cols
 
 
 def linear_fused(x, w, bias=None, act: str = "none", residual=None, out=None, out_dtype=None, status=None, stream=None):
@@ -388,40 +406,44 @@ def linear_fused(x, w, bias=None, act: str = "none", residual=None, out=None, ou
     ACTIVATIONS; residual [M, N] of out's dtype (a stride-0 row broadcasts); out [M, N] of x's
     dtype or float32, residual itself for an update in place; status int32 [1] (zeroed) receives
     a timeout.  Returns out."""
-    lib = load()
+    rt, name = _RT or _rt(), "linear_fused"
     _need(x.dim() == 2 and w.dim() == 2 and x.shape[1] == w.shape[1], "linear_fused: x [M, K] and w [N, K]")
-    (M, K), N = x.shape, w.shape[0]
-    code = _dtype_code(x.dtype, False, "linear_fused")
-    _need(w.dtype == x.dtype, "linear_fused: x and w of one dtype")
-    if act not in ACTIVATIONS:
+    (M, K), N, dtype = x.shape, w.shape[0], x.dtype
+    code = rt.code16.get(dtype)
+    if code is None:
+        _no_dtype(name, dtype)
+    _need(w.dtype == dtype, "linear_fused: x and w of one dtype")
+    a = ACTIVATIONS.get(act)
+    if a is None:
         raise ValueError(f"linear_fused: act {act!r} is none of {sorted(ACTIVATIONS)}")
-    if out is None:
-        out = _fresh((M, N), x.dtype if out_dtype is None else out_dtype, x.device, stream)
-    _need(tuple(out.shape) == (M, N) and (out_dtype is None or out.dtype == out_dtype),
-          "linear_fused: out [M, N] of out_dtype")
-    ocode = _dtype_code(out.dtype, True, "linear_fused")
-    _need(_last1(x) and _last1(w) and _last1(out), "linear_fused: last strides must be 1")
+    odtype = (dtype if out is None else out.dtype) if out_dtype is None else out_dtype
+    ocode = rt.code.get(odtype)
+    if ocode is None:
+        _no_dtype(name, odtype)
     if bias is not None:
-        _need(bias.shape == (N,) and _DTYPE_CODES.get(bias.dtype) == DIT_DTYPE_F32 and _last1(bias),
-              "linear_fused: bias float32 [N]")
-    ldr = 0
+        _need(bias.shape == (N,) and bias.dtype == rt.float32 and bias.is_contiguous(), "linear_fused: bias float32 [N]")
+    ldx, ldw, ldr = _row_stride(x, name), _row_stride(w, name), 0
+    if out is None:
+        out, ldy = _fresh(x, (M, N), odtype, stream), N
+    else:
+        _need(out.shape == (M, N) and out.dtype == odtype, "linear_fused: out [M, N] of out_dtype")
+        ldy = _row_stride(out, name)
     if residual is not None:
-        _need(residual.shape == out.shape and residual.dtype == out.dtype and _last1(residual),
+        _need(residual.shape == (M, N) and residual.dtype == odtype and (residual.stride(1) == 1 or N == 1),
               "linear_fused: residual [M, N] of out's dtype")
         ldr = residual.stride(0)
-    _call(lib.dit_op_linear_fused, "linear_fused", (x, w, out, bias, residual, status), stream, code, x.data_ptr(),
-          x.stride(0) if M > 1 else 0, w.data_ptr(), w.stride(0) if N > 1 else 0, _ptr(bias), ACTIVATIONS[act],
-          _ptr(residual), ldr, out.data_ptr(), out.stride(0) if M > 1 else N, ocode, M, N, K, _ptr(status))
+    _enqueue(rt, name, rt.lib.dit_op_linear_fused, (x, w, out, bias, residual, status), stream,
+             (code, x.data_ptr(), ldx, w.data_ptr(), ldw, None if bias is None else bias.data_ptr(), a,
+              None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy, ocode, M, N, K, _ptr(status)))
     return out
 
 
-def _last1(t) -> bool:
-    return t.stride(-1) == 1 or t.shape[-1] == 1
-
-
-def _strides(t):
+def _head_strides(t, name: str):
     """Token and head stride of [tokens, heads, features]; those of a length-1 axis are free."""
     n, h, d = t.shape
+    if t.is_contiguous():
+        return h * d, d
+    _need(d == 1 or t.stride(2) == 1, name + ": last strides must be 1")
     sh = t.stride(1) if h > 1 else -(-d // 8) * 8
     return (t.stride(0) if n > 1 else h * sh), sh
 
@@ -435,32 +457,28 @@ def attention_packed(q, k, v, cu_q, cu_k, max_q: int, max_k: int, causal: bool =
     lengths; causal aligns the last query with the last key; scale defaults to dh^-0.5.
     Returns out (rows outside every sequence are not written; a new out starts undefined
     there), or (out, lse float32 [heads, total_q]) with return_lse."""
-    lib = load()
-    _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3 and k.shape == v.shape and q.shape[2] == k.shape[2],
+    rt, name = _RT or _rt(), "attention_packed"
+    _need(q.dim() == 3 and k.dim() == 3 and k.shape == v.shape and q.shape[2] == k.shape[2],
           "attention_packed: q [total_q, heads, dh], k and v [total_k, kv_heads, dh]")
-    (tq, h, d), (tk, hk, _) = q.shape, k.shape
-    code = _dtype_code(q.dtype, False, "attention_packed")
-    _need(k.dtype == q.dtype and v.dtype == q.dtype, "attention_packed: q, k and v of one dtype")
-    if out is None:
-        out = _fresh((tq, h, d), q.dtype, q.device, stream)
-    _need(out.shape == q.shape and out.dtype == q.dtype, "attention_packed: out like q")
-    _need(_last1(q) and _last1(k) and _last1(v) and _last1(out), "attention_packed: last strides must be 1")
+    (tq, h, d), (tk, hk, _), dtype = q.shape, k.shape, q.dtype
+    code = rt.code16.get(dtype)
+    if code is None:
+        _no_dtype(name, dtype)
+    _need(k.dtype == dtype and v.dtype == dtype, "attention_packed: q, k and v of one dtype")
     n = cu_q.shape[0] - 1
-    _need(cu_q.dim() == 1 and n >= 0 and cu_k.shape == cu_q.shape and cu_q.is_contiguous() and cu_k.is_contiguous()
-          and not (cu_q.dtype.is_floating_point or cu_k.dtype.is_floating_point) and cu_q.element_size() == 4
-          and cu_k.element_size() == 4, "attention_packed: cu_q and cu_k contiguous int32 [n + 1]")
-    lse = _fresh((h, tq), _f32(), q.device, stream) if return_lse else None
-    strides = (c_longlong * 8)(*_strides(q), *_strides(k), *_strides(v), *_strides(out))
-    _call(lib.dit_op_attention_packed, "attention_packed", (q, k, v, out, lse, cu_q, cu_k, status), stream, code,
-          q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), cu_q.data_ptr(), cu_k.data_ptr(), n, tq,
-          tk, int(max_q), int(max_k), h, hk, d, strides, float(d ** -0.5 if scale is None else scale), int(causal),
-          _ptr(status))
+    _need(cu_q.dim() == 1 and n >= 0 and cu_k.shape == cu_q.shape and cu_q.dtype == rt.int32 and cu_k.dtype == rt.int32
+          and cu_q.is_contiguous() and cu_k.is_contiguous(), "attention_packed: cu_q and cu_k contiguous int32 [n + 1]")
+    if out is None:
+        out = _fresh(q, (tq, h, d), dtype, stream)
+    else:
+        _need(out.shape == q.shape and out.dtype == dtype, "attention_packed: out like q")
+    strides = _Strides8(*_head_strides(q, name), *_head_strides(k, name), *_head_strides(v, name), *_head_strides(out, name))
+    lse = _fresh(q, (h, tq), rt.float32, stream) if return_lse else None
+    _enqueue(rt, name, rt.lib.dit_op_attention_packed, (q, k, v, out, lse, cu_q, cu_k, status), stream,
+             (code, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+              cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q, max_k, h, hk, d, strides,
+              d ** -0.5 if scale is None else scale, 1 if causal else 0, _ptr(status)))
     return (out, lse) if return_lse else out
-
-
-def _f32():
-    import torch
-    return torch.float32
 
 
 class Rotary:
@@ -472,8 +490,8 @@ class Rotary:
     def __init__(self, head_dim: int, rotary_dim: Optional[int] = None, interleaved: bool = False,
                  base: float = 10000.0, axes: int = 1, scaling: str = "none", factor: float = 1.0,
                  original_length: int = 0, freqs: Optional[Sequence[float]] = None):
-        self.lib = load()
-        self.head_dim, self.axes, self.interleaved = int(head_dim), int(axes), bool(interleaved)
+        lib = load()
+        self.head_dim, self.axes, self.interleaved = int(head_dim), int(axes), int(bool(interleaved))
         part = self.head_dim if rotary_dim is None else int(rotary_dim)
         _need(self.axes > 0 and 0 < part <= self.head_dim and part % (2 * self.axes) == 0,
               "Rotary: rotary_dim must be a multiple of 2 * axes and at most head_dim")
@@ -485,11 +503,10 @@ class Rotary:
             _need(len(freqs) == each, f"Rotary: freqs needs {each} entries")
             f[:] = [float(v) for v in freqs]
         else:
-            self._check(self.lib.dit_rotary_frequencies(ROTARY_SCALINGS[scaling], each, float(base), float(factor),
-                                                        int(original_length), f, ctypes.byref(amp)),
-                        "dit_rotary_frequencies")
+            self._check(lib.dit_rotary_frequencies(ROTARY_SCALINGS[scaling], each, float(base), float(factor),
+                                                   int(original_length), f, ctypes.byref(amp)), "dit_rotary_frequencies")
         self._plan = RotaryPlan()
-        self._check(self.lib.dit_rotary_init(ctypes.byref(self._plan), f, each, self.axes, amp), "dit_rotary_init")
+        self._check(lib.dit_rotary_init(ctypes.byref(self._plan), f, each, self.axes, amp), "dit_rotary_init")
         self._ref = ctypes.byref(self._plan)
 
     @staticmethod
@@ -501,20 +518,22 @@ class Rotary:
         """x [tokens, heads, head_dim] (float32, bf16 or fp16) turned by positions [tokens] or
         [tokens, axes] (int32 or int64); out=x turns in place.  transpose: the gradient of x
         from that of the result."""
+        rt, name = _RT or _rt(), "Rotary.apply"
         _need(x.dim() == 3 and x.shape[2] == self.head_dim, "Rotary.apply: x [tokens, heads, head_dim]")
-        code = _dtype_code(x.dtype, True, "Rotary.apply")
-        if out is None:
-            out = _fresh(tuple(x.shape), x.dtype, x.device, stream)
-        _need(out.shape == x.shape and out.dtype == x.dtype and _last1(x) and _last1(out),
-              "Rotary.apply: out like x, last strides 1")
-        n = x.shape[0]
-        _need(positions.is_contiguous() and not positions.dtype.is_floating_point
-              and positions.element_size() in (4, 8)
+        (n, h, d), code = x.shape, rt.code.get(x.dtype)
+        if code is None:
+            _no_dtype(name, x.dtype)
+        wide = positions.dtype == rt.int64
+        _need((wide or positions.dtype == rt.int32) and positions.is_contiguous()
               and (positions.shape == (n, self.axes) or (self.axes == 1 and positions.shape == (n,))),
               "Rotary.apply: positions contiguous int32 or int64 [tokens, axes]")
-        xt, xh = _strides(x)
-        yt, yh = _strides(out)
-        _call(self.lib.dit_op_rotary, "Rotary.apply", (x, positions, out), stream, self._ref, code, x.data_ptr(), xt, xh,
-              positions.data_ptr(), int(positions.element_size() == 8), out.data_ptr(), yt, yh, n, x.shape[1],
-              self.head_dim, int(self.interleaved), int(transpose))
+        xt, xh = _head_strides(x, name)
+        if out is None:
+            out, yt, yh = _fresh(x, (n, h, d), x.dtype, stream), h * d, d
+        else:
+            _need(out.shape == x.shape and out.dtype == x.dtype, "Rotary.apply: out like x")
+            yt, yh = _head_strides(out, name)
+        _enqueue(rt, name, rt.lib.dit_op_rotary, (x, positions, out), stream,
+                 (self._ref, code, x.data_ptr(), xt, xh, positions.data_ptr(), 1 if wide else 0, out.data_ptr(), yt, yh, n, h,
+                  d, self.interleaved, 1 if transpose else 0))
         return out

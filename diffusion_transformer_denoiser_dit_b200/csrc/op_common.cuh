@@ -61,10 +61,25 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(e));
   return e != 0;
 }
-// mbar_wait by a whole warp: false for every lane when it ran out for any
+// mbar_wait that looks at the clock only once in 1024 tries: a read of globaltimer between two
+// tries costs more than most waits last.
+__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, int* status) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        record_status(status, DIT_ERR_DEVICE_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+// The same by a whole warp: false for every lane when it ran out for any.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* status) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+  return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, status));
 }
 
 // Instruction descriptor, kind::f16: A and B both fp16 or both bf16, K-major, f32 accumulator.

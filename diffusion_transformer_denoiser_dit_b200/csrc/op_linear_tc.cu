@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(384, 1)
       const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
       if constexpr (F32) {
         for (int kb0 = 0; kb0 < kblocks; kb0 += chunk, ++it) {
-          ok = mbar_wait(TFULL(it & 1), (it >> 1) & 1, a.status);
+          ok = mbar_wait_spin(TFULL(it & 1), (it >> 1) & 1, a.status);
           __syncwarp();
           if (__any_sync(0xffffffffu, !ok)) {
             ok = false;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(384, 1)
           mbar_arrive_cluster(mapa_shared(TEMPTY(it & 1), 0));
         }
       } else {
-        ok = mbar_wait(TFULL(it & 1), (it >> 1) & 1, a.status);
+        ok = mbar_wait_spin(TFULL(it & 1), (it >> 1) & 1, a.status);
         __syncwarp();
         ok = !__any_sync(0xffffffffu, !ok);
         tc_fence_after();
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(384, 1)
         });
         if (tma_out) {
           if (res_tma) {
-            ok = mbar_wait(RES(w, b), (use >> 1) & 1, a.status);
+            ok = mbar_wait_spin(RES(w, b), (use >> 1) & 1, a.status);
             __syncwarp();
             if (__any_sync(0xffffffffu, !ok)) {
               ok = false;
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(192)
       int s = 0;
       uint32_t ph = 0;
       for (int kb = kb_begin; kb < kb_end; ++kb) {
-        if (!mbar_wait(EMPTY(s), ph ^ 1u, a.status)) break;
+        if (!mbar_wait_spin(EMPTY(s), ph ^ 1u, a.status)) break;
         uint8_t* sa = smem + s * C::STAGE;
         if (sp.grain_x) gather_tile(sa, static_cast<const T*>(a.x), a.ldx, m0, a.M, kb * 64, a.K, 128, sp.grain_x, tid);
         if (sp.grain_w)
