@@ -41,8 +41,6 @@ constexpr int kPolyEvery = 4;
 
 template <int NA, bool SPLIT>
 struct FaCfg {
-  static constexpr bool ALIAS = NA == 2;             // P takes the place of S in TMEM (O needs the rest)
-  static constexpr int P1 = ALIAS ? 64 : 32;         // columns from P of keys 0-63 to P of keys 64-127
   static constexpr int ATOM = 128 * 128;             // 128 rows x 64 features
   static constexpr int TILE = NA * ATOM;
   static constexpr int QT = SPLIT ? 1 : 2;           // query tiles per item
@@ -71,7 +69,7 @@ struct FaItem {
 template <int NA, bool SPLIT>
 struct FaBars {
   using C = FaCfg<NA, SPLIT>;
-  enum { IF = 0, IE = 2, QF = 4, QE = 6, SF = 8, SR = 10, PF = 12, OD = 14, OF = 16, KF = 18, KE = KF + C::SLOTS, N = KE + C::SLOTS };
+  enum { IF = 0, IE = 2, QF = 4, QE = 6, SF = 8, PF = 10, OD = 12, OF = 14, KF = 16, KE = KF + C::SLOTS, N = KE + C::SLOTS };
   static_assert(8 * N + 16 + 2 * sizeof(FaItem) <= 448, "barrier area");
 };
 
@@ -91,12 +89,13 @@ __device__ __forceinline__ void mma_qk(uint32_t tS, uint32_t qd, uint32_t kd, ui
     mma_bf16_ss(tS, sdesc_make(qd + o, kSdescHiSw128), sdesc_make(kd + o, kSdescHiSw128), idesc, k > 0 ? 1u : 0u);
   }
 }
-// O (+)= P V over STEPS x 16 keys; P1 columns from P of the first 64 keys to the others
-template <int STEPS, int P1>
+// O (+)= P V over STEPS x 16 keys; P of keys 64-127 starts 64 columns behind P of keys 0-63, each in
+// the place of its own scores
+template <int STEPS>
 __device__ __forceinline__ void mma_pv(uint32_t tO, uint32_t tP, uint32_t vd, uint32_t idesc, uint32_t more) {
 #pragma unroll
   for (int k = 0; k < STEPS; ++k)
-    mma_bf16_ts(tO, tP + (k >> 2) * P1 + 8 * (k & 3), sdesc_make(vd + k * (2048 >> 4), kSdescHiSw128), idesc, k > 0 ? 1u : more);
+    mma_bf16_ts(tO, tP + (k >> 2) * 64 + 8 * (k & 3), sdesc_make(vd + k * (2048 >> 4), kSdescHiSw128), idesc, k > 0 ? 1u : more);
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
@@ -153,7 +152,6 @@ __global__ void __launch_bounds__(640, 1)
       mbar_init(bar(B::QF + i), 1);
       mbar_init(bar(B::QE + i), 1);
       mbar_init(bar(B::SF + i), 1);
-      mbar_init(bar(B::SR + i), 8);               // the group's warps have S in registers
       mbar_init(bar(B::PF + i), 8);               // the group's warps have written P
       mbar_init(bar(B::OD + i), 1);
       mbar_init(bar(B::OF + i), 8);
@@ -213,39 +211,43 @@ __global__ void __launch_bounds__(640, 1)
       const uint32_t q_bytes = static_cast<uint32_t>(f.G * f.TQ) * 128;
       bool ok = true;
       for (int n = 0; next_item(n, it); ++n) {
-        const int qb = n % C::QB;
+        const int j0 = SPLIT ? it.t0 : 0, j1 = SPLIT ? it.t1 : max(it.t0, it.t1);
+        auto load_tile = [&](int r, int j, const CUtensorMap* map) {
+          const int at = r * C::RS + slot[r];
+          ok = ok && mbar_wait_warp(bar(B::KE + at), ph[r] ^ 1u, a.status);
+          if (ok && elect_one()) {
+            mbar_arrive_expect_tx(bar(B::KF + at), C::TILE);
+#pragma unroll
+            for (int c = 0; c < NA; ++c)
+              tma_load_3d(sbase + C::OFF_KV + at * C::TILE + c * C::ATOM, map, bar(B::KF + at), c * 64, it.hk, it.k0 + j * 128);
+          }
+          __syncwarp();
+          if (++slot[r] == C::RS) {
+            slot[r] = 0;
+            ph[r] ^= 1u;
+          }
+        };
+        // K of the first tile before Q: its slot is free earlier than Q's place
+        if (j0 < j1) load_tile(0, j0, &tmK);
+        const int qb = n % C::QB, ng = !SPLIT && it.ntok > f.TQ ? 2 : 1;
         ok = ok && mbar_wait_warp(bar(B::QE + qb), ((n / C::QB) & 1) ^ 1, a.status);
-        const int ng = !SPLIT && it.ntok > f.TQ ? 2 : 1;
         if (ok && elect_one()) {
           mbar_arrive_expect_tx(bar(B::QF + qb), ng * NA * q_bytes);
           for (int g = 0; g < ng; ++g)
+#pragma unroll
             for (int c = 0; c < NA; ++c)
               tma_load_3d(sbase + (qb * C::QT + g) * C::TILE + c * C::ATOM, &tmQ, bar(B::QF + qb), c * 64, it.hk * f.G,
                           it.tok0 + g * f.TQ);
         }
         __syncwarp();
-        const int j0 = SPLIT ? it.t0 : 0, j1 = SPLIT ? it.t1 : max(it.t0, it.t1);
-        for (int j = j0; j < j1 && ok; ++j) {
-          const int r = SPLIT ? (j - j0) & 1 : 0;
+        if (j0 < j1) load_tile(0, j0, &tmV);
+        for (int j = j0 + 1; j < j1; j += C::RINGS) {
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            int& s = slot[C::RINGS == 2 ? r : 0];
-            uint32_t& p = ph[C::RINGS == 2 ? r : 0];
-            const int at = r * C::RS + s;
-            if (!mbar_wait_warp(bar(B::KE + at), p ^ 1u, a.status)) {
-              ok = false;
-              break;
-            }
-            if (elect_one()) {
-              mbar_arrive_expect_tx(bar(B::KF + at), C::TILE);
-              for (int c = 0; c < NA; ++c)
-                tma_load_3d(sbase + C::OFF_KV + at * C::TILE + c * C::ATOM, kv ? &tmV : &tmK, bar(B::KF + at), c * 64, it.hk,
-                            it.k0 + j * 128);
-            }
-            __syncwarp();
-            if (++s == C::RS) {
-              s = 0;
-              p ^= 1u;
+          for (int r = 0; r < C::RINGS; ++r) {  // split form: the second ring is due first
+            const int at = C::RINGS == 2 ? 1 - r : 0;
+            if (j + r < j1) {
+              load_tile(at, j + r, &tmK);
+              load_tile(at, j + r, &tmV);
             }
           }
         }
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(640, 1)
       constexpr uint32_t idesc_s = idesc_16<T>(128, 128);
       const int n16 = (a.dh + 15) / 16;
       const uint32_t idesc_o = idesc_16<T>(128, 16 * n16) | (1u << 16);  // B (V) is MN-major
-      int ns[2] = {}, np[2] = {}, ni[2] = {};  // per group: QK and PV issued; items with tiles
+      int np[2] = {}, ni[2] = {};  // per group: PV issued; items with tiles
       bool ok = true;
       // K and V alternate in a ring: K of tile j + 1 lies two slots behind K of tile j, V of tile j between
       int kslot[C::RINGS] = {}, vslot[C::RINGS];
@@ -356,9 +358,7 @@ __global__ void __launch_bounds__(640, 1)
         wait(bar(B::QF + qb), (n / C::QB) & 1);
         // S_g = Q_g K_j from the slot `at`
         auto issue_qk = [&](int g, int at) {
-          // without aliasing S is free once the softmax has the previous one in registers; with it,
-          // the product that reads P in its place was issued before this one
-          if (!C::ALIAS && ns[g] > 0) wait(bar(B::SR + g), (ns[g] - 1) & 1);
+          // S is free: the product that reads P in its place was issued before this one
           tc_fence_after();
           const uint32_t qd = sdesc_lo(sbase + (qb * C::QT + (SPLIT ? 0 : g)) * C::TILE);
           const uint32_t kd = sdesc_lo(sbase + C::OFF_KV + at * C::TILE), tS = tmem_base + g * 128;
@@ -373,7 +373,6 @@ __global__ void __launch_bounds__(640, 1)
             mma_commit(bar(B::SF + g));
           }
           __syncwarp();
-          ++ns[g];
         };
         // O_g (+)= P_g V_j from the slot `at`, whose keys start at key0
         auto issue_pv = [&](int g, int at, int j, int key0) {
@@ -382,17 +381,17 @@ __global__ void __launch_bounds__(640, 1)
           const int steps = min(8, (it.nk - key0 + 15) >> 4);
           const uint32_t vd = sdesc_mn_lo(sbase + C::OFF_KV + at * C::TILE);
           const uint32_t tO = tmem_base + 256 + g * (NA == 1 ? 64 : 128);
-          const uint32_t tP = C::ALIAS ? tmem_base + g * 128 : tmem_base + 384 + g * 64;
+          const uint32_t tP = tmem_base + g * 128;
           wait(bar(B::PF + g), np[g] & 1);
           tc_fence_after();
           if (ok && elect_one()) {
             const uint32_t more = j > 0 ? 1u : 0u;
             if (steps == 8) {
-              mma_pv<8, C::P1>(tO, tP, vd, idesc_o, more);
+              mma_pv<8>(tO, tP, vd, idesc_o, more);
             } else {
-              mma_pv<1, C::P1>(tO, tP, vd, idesc_o, more);
+              mma_pv<1>(tO, tP, vd, idesc_o, more);
               for (int k = 1; k < steps; ++k)
-                mma_pv<1, C::P1>(tO, tP + (k >> 2) * C::P1 + 8 * (k & 3), vd + k * (2048 >> 4), idesc_o, 1u);
+                mma_pv<1>(tO, tP + (k >> 2) * 64 + 8 * (k & 3), vd + k * (2048 >> 4), idesc_o, 1u);
             }
             mma_commit(bar(B::OD + g));
           }
@@ -431,15 +430,15 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               if (j >= mine[g]) continue;
-              if (!C::ALIAS && j + 1 < mine[g]) k_of(g);
               const int at = g * C::RS + vslot[g % C::RINGS], key0 = (it.t0 + 2 * j + g) * 128;
               wait(bar(B::KF + at), vph[g % C::RINGS]);
               clear_tail(at, key0);
               issue_pv(g, at, j, key0);
               release(bar(B::KE + at));
               step2(vslot[g % C::RINGS], vph[g % C::RINGS]);
-              if (C::ALIAS && j + 1 < mine[g]) k_of(g);
+              if (j + 1 < mine[g]) k_of(g);
             }
+            if (j + 2 == all) release(bar(B::QE + qb));  // that was Q's last product
           }
         } else {
           if (all > 0) {
@@ -457,9 +456,8 @@ __global__ void __launch_bounds__(640, 1)
             clear_tail(vat, j * 128);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              if (!C::ALIAS && j + 1 < mine[g]) issue_qk(g, kat);
               if (j < mine[g]) issue_pv(g, vat, j, j * 128);
-              if (C::ALIAS && j + 1 < mine[g]) issue_qk(g, kat);
+              if (j + 1 < mine[g]) issue_qk(g, kat);
             }
             release(bar(B::KE + vat));
             step2(vslot[0], vph[0]);
@@ -467,9 +465,10 @@ __global__ void __launch_bounds__(640, 1)
               release(bar(B::KE + kat));
               step2(kslot[0], kph[0]);
             }
+            if (j + 2 == all) release(bar(B::QE + qb));  // that was Q's last product
           }
         }
-        release(bar(B::QE + qb));
+        if (all <= 1) release(bar(B::QE + qb));
 #pragma unroll
         for (int g = 0; g < 2; ++g) ni[g] += mine[g] > 0;
         exchange_others();
@@ -483,7 +482,6 @@ __global__ void __launch_bounds__(640, 1)
     const int g = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, q = warp & 3, r = q * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t tS = tmem_base + lane_off + g * 128 + hf * 64, tO = tmem_base + lane_off + 256 + g * (NA == 1 ? 64 : 128);
-    const uint32_t tP = C::ALIAS ? tS : tmem_base + lane_off + 384 + g * 64 + hf * 32;
     const int rt = r / f.G, rh = r - rt * f.G;  // token and head of this row within the tile
     const uint32_t pair = 1 + g * 4 + q;        // named barrier of the two warps that share 32 rows
     volatile float* row = reinterpret_cast<volatile float*>(smem + C::OFF_ROW) + g * 128 + r;
@@ -509,11 +507,6 @@ __global__ void __launch_bounds__(640, 1)
         const int key0 = (SPLIT ? it.t0 + 2 * j + g : j) * 128 + hf * 64;
         if (!mbar_wait_warp(bar(B::SF + g), cnt & 1, a.status)) ok = false;
         if (!warp_ok) {
-          if (!C::ALIAS) {
-            if (elect_one()) mbar_arrive(bar(B::SR + g));
-            // this S may be there before the previous P is: no warp arrives for two tiles at once
-            if (ok && j > 0 && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) ok = false;
-          }
           __syncwarp();
           if (elect_one()) mbar_arrive(bar(B::PF + g));
           __syncwarp();
@@ -524,12 +517,6 @@ __global__ void __launch_bounds__(640, 1)
         tmem_ld32(tS, s);
         tmem_ld32(tS + 32, s + 32);
         tmem_ld_wait<64>(s);
-        if (!C::ALIAS) {
-          tc_fence_before();
-          __syncwarp();
-          if (elect_one()) mbar_arrive(bar(B::SR + g));
-          __syncwarp();
-        }
         const int nvalid = lim - key0;
         if (__any_sync(0xffffffffu, nvalid < 64)) {
 #pragma unroll
@@ -552,10 +539,8 @@ __global__ void __launch_bounds__(640, 1)
           m_ref = m_new;
           l *= alpha;
           if (j > 0) {
-            // O moves to the new maximum, each half every other 16 columns.  Its last product is complete:
-            // with aliasing it came before this S in the same pipe, otherwise its barrier says so.
-            if (!C::ALIAS && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) ok = false;
-            tc_fence_after();
+            // O moves to the new maximum, each half every other 16 columns.  Its last product is complete: it
+            // came before this S in the same pipe.
 #pragma unroll 1
             for (int c = 16 * hf; c < a.dh; c += 32) {
               uint32_t o[16];
@@ -570,8 +555,6 @@ __global__ void __launch_bounds__(640, 1)
             named_barrier_sync(pair, 64);  // all of O before either half's P lets the next product start
           }
         }
-        // P's place is free once the previous product has read it (with aliasing: it has)
-        if (!C::ALIAS && j > 0 && !mbar_wait_warp(bar(B::OD + g), (cnt - 1) & 1, a.status)) ok = false;
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen no key yet
         const uint64_t sc2 = f2_pack(f.sc, f.sc), nm2 = f2_pack(-mu, -mu);
         uint64_t rs2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
@@ -594,7 +577,7 @@ __global__ void __launch_bounds__(640, 1)
           f2_unpack(p2, p0, p1);
           pk[i - 16 * h] = pack2<T>(p0, p1);
         }
-        tmem_st16(tP + 16 * h, pk);
+        tmem_st16(tS + 16 * h, pk);  // P, in the place of S
         }
         tmem_st_wait();
         tc_fence_before();
@@ -614,21 +597,43 @@ __global__ void __launch_bounds__(640, 1)
       if constexpr (!SPLIT) {
         if (warp_ok) {
           const float inv = lim > 0 ? 1.0f / l : 0.f;
-          T* out = static_cast<T*>(a.o) + (it.tok0 + tok) * a.o_tok + head * a.o_head;
+          // 32 columns at a time (each half every other 32): a lane's row is four 16-byte units; four lanes
+          // exchange them so that lane i of the four holds unit i of their four rows, and a store covers
+          // 64 bytes of each of eight rows instead of 16 of 32
+          const long long row_at = row_ok ? (it.tok0 + tok) * a.o_tok + head * a.o_head : -1;
+          const int sub = lane & 3;
 #pragma unroll 1
-          for (int c = 16 * hf; c < a.dh; c += 32) {
-            uint32_t o[16];
+          for (int c = 32 * hf; c < a.dh; c += 64) {
+            uint32_t u[4][4];
             if (mine > 0) {
-              tmem_ld16(tO + c, o);
-              tmem_ld_wait<16>(o);
-            }
-            if (row_ok) {
-              uint32_t p[8];
+              uint32_t o[32];
+              tmem_ld32(tO + c, o);
+              tmem_ld_wait<32>(o);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                p[i] = lim > 0 ? pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
-              *reinterpret_cast<uint4*>(out + c) = make_uint4(p[0], p[1], p[2], p[3]);
-              if (c + 8 < a.dh) *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+              for (int i = 0; i < 16; ++i)
+                u[i >> 2][i & 3] = lim > 0 ? pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) u[i >> 2][i & 3] = 0u;
+            }
+#pragma unroll
+            for (int x = 1; x < 4; x <<= 1)  // swap unit i ^ x of this lane with unit i of lane ^ x
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (!(i & x))
+#pragma unroll
+                  for (int w = 0; w < 4; ++w) {
+                    const bool up = sub & x;
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? u[i][w] : u[i ^ x][w], x);
+                    if (up) u[i][w] = got;
+                    else u[i ^ x][w] = got;
+                  }
+            // u[i] is now unit `sub` of the row of lane (lane & ~3) + i
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const long long at = __shfl_sync(0xffffffffu, row_at, (lane & ~3) + i);
+              if (at >= 0 && c + 8 * sub < a.dh)
+                *reinterpret_cast<uint4*>(static_cast<T*>(a.o) + at + c + 8 * sub) = make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]);
             }
           }
           if (row_ok && hf == 0 && a.lse)
@@ -644,11 +649,12 @@ __global__ void __launch_bounds__(640, 1)
         // of CTA c, group g is slot 2 c + g: O rows [slot][row][16 n16] float32, then (max, sum) [slot][row].
         cluster_sync_all();
         const int rows = min(f.TQ, it.ntok) * f.G, share = (rows + f.split - 1) / f.split;
-        const int wide = (a.dh + 15) / 16 * 64;  // bytes of a row
+        const uint32_t wide = (a.dh + 15) / 16 * 64;  // bytes of a row
         const uint32_t part = sbase + C::OFF_KV, stats = part + 2 * f.split * share * wide;
         if (q * 32 < rows) {
           const int owner = min(r / share, f.split - 1), pr = (2 * rank + g) * share + r - owner * share;
-          const uint32_t peer = mapa_shared(part, owner) + pr * wide;
+          // a row's 16-byte units are rotated by its number: neighbouring rows meet other banks
+          const uint32_t peer = mapa_shared(part, owner) + pr * wide, turn = (pr * 16) % wide;
 #pragma unroll 1
           for (int c = 16 * hf; c < a.dh && mine > 0; c += 32) {
             uint32_t o[16];
@@ -656,7 +662,11 @@ __global__ void __launch_bounds__(640, 1)
             tmem_ld_wait<16>(o);
             if (r < rows)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) st_cluster_v4(peer + c * 4 + i * 16, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              for (int i = 0; i < 4; ++i) {
+                uint32_t at = c * 4 + i * 16 + turn;
+                if (at >= wide) at -= wide;
+                st_cluster_v4(peer + at, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              }
           }
           if (r < rows && hf == 0) st_cluster_v2(mapa_shared(stats, owner) + pr * 8, m_ref, l);
         }
@@ -680,8 +690,11 @@ __global__ void __launch_bounds__(640, 1)
             if (st.x == -INFINITY) continue;  // nothing seen: its O row was not written
             const float w = ex2_approx(st.x - mx);
             sum += w * st.y;
-            const float4* src = reinterpret_cast<const float4*>(gp + (p * share + lr) * wide + u * 32);
-            const float4 x = src[0], y = src[1];
+            const uint32_t pr = p * share + lr, turn = (pr * 16) % wide;
+            uint32_t a0 = u * 32 + turn, a1 = a0 + 16;
+            if (a0 >= wide) a0 -= wide;
+            if (a1 >= wide) a1 -= wide;
+            const float4 x = *reinterpret_cast<const float4*>(gp + pr * wide + a0), y = *reinterpret_cast<const float4*>(gp + pr * wide + a1);
             o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
             o[4] += w * y.x, o[5] += w * y.y, o[6] += w * y.z, o[7] += w * y.w;
           }
