@@ -48,14 +48,22 @@ struct FaCfg {
   static constexpr int Q_BYTES = QB * QT * TILE;
   static constexpr int SLOTS = (224 * 1024 - Q_BYTES) / TILE;  // K / V tiles in flight, all rings
   static constexpr int RINGS = SPLIT ? 2 : 1;
-  static constexpr int RS = SLOTS / RINGS;           // slots per ring
+  static constexpr int RS = SPLIT ? (SLOTS - 2) / 2 : SLOTS;   // slots per ring; the split form keeps two for
+  static constexpr int OFF_X = Q_BYTES + RINGS * RS * TILE;    // the exchange of few rows
   static constexpr int OFF_KV = Q_BYTES;
   static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
-  static constexpr int OFF_ROW = OFF_BAR + 448;      // one float per query row: the halves' exchange
+  static constexpr int OFF_SORT = OFF_BAR + 448;     // 32 lane numbers
+  static constexpr int OFF_ROW = OFF_SORT + 128;      // one float per query row: the halves' exchange
   static constexpr int SMEM = 1024 + OFF_ROW + 1024;
   static constexpr int THREADS = 640, REG_CTRL = 64, REG_SOFTMAX = 104;
   static constexpr int REG_POOL = 128 * REG_CTRL + 512 * REG_SOFTMAX;
-  static_assert(SMEM <= 232448 && RS >= 3, "shared memory");
+  static_assert(SMEM <= 232448 && RS >= 2, "shared memory");
+  // split form with at most this many rows per tile: the partial rows of one item, two groups of up to
+  // eight CTAs with the rows rounded up to a multiple of the CTAs, fit one slot
+  static constexpr int LIGHT_ROWS = 24;
+  static_assert(LIGHT_ROWS % 8 == 0 && 2 * LIGHT_ROWS * (NA * 256 + 8) <= TILE, "exchange slot");
+  // with all 128 rows: all slots
+  static_assert(2 * 128 * (NA * 256 + 8) <= SLOTS * TILE, "exchange of a full tile");
 };
 
 struct FaItem {
@@ -69,7 +77,7 @@ struct FaItem {
 template <int NA, bool SPLIT>
 struct FaBars {
   using C = FaCfg<NA, SPLIT>;
-  enum { IF = 0, IE = 2, QF = 4, QE = 6, SF = 8, PF = 10, OD = 12, OF = 14, KF = 16, KE = KF + C::SLOTS, N = KE + C::SLOTS };
+  enum { IF = 0, IE = 2, QF = 4, QE = 6, SF = 8, PF = 10, OD = 12, OF = 14, XF = 16, KF = 18, KE = KF + C::SLOTS, N = KE + C::SLOTS };
   static_assert(8 * N + 16 + 2 * sizeof(FaItem) <= 448, "barrier area");
 };
 
@@ -122,10 +130,24 @@ __device__ __forceinline__ bool any_of_pair(uint32_t id, bool v) {
   return any != 0;
 }
 
+__device__ __forceinline__ float2 ld_shared_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// wait for arrivals from other CTAs of the cluster and see what they wrote before them
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int* status) {
+  const bool ok = mbar_wait_warp(bar, parity, status);
+  fence_cluster();
+  return ok;
+}
+
 struct FaArgs {
   PackedAttnArgs a;
   int G, TQ;        // heads per key head, query tokens per tile
   int split;        // CTAs per cluster (split form)
+  int light;        // split form with few rows per tile
   float sc;         // scale * log2(e)
 };
 
@@ -155,6 +177,7 @@ __global__ void __launch_bounds__(640, 1)
       mbar_init(bar(B::PF + i), 8);               // the group's warps have written P
       mbar_init(bar(B::OD + i), 1);
       mbar_init(bar(B::OF + i), 8);
+      mbar_init(bar(B::XF + i), 4 * f.split);     // partial rows of the cluster's four warps that have rows
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(bar(B::KF + i), 1);
@@ -167,7 +190,12 @@ __global__ void __launch_bounds__(640, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (SPLIT) {  // the barriers are there before another CTA of the cluster arrives on them
+    __syncwarp();
+    cluster_sync_all();
+  } else {
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem_base = uniform(*holder);
   pdl_trigger();
@@ -192,9 +220,9 @@ __global__ void __launch_bounds__(640, 1)
     }
     __syncwarp();
   };
-  // split form: partial rows are exchanged through the K / V slots once every CTA is done with them
+  // split form, many rows: they are exchanged through the K / V slots once every CTA is done with them
   auto exchange_others = [&]() {
-    if constexpr (SPLIT) {
+    if (SPLIT && !f.light) {
       __syncwarp();
       cluster_sync_all();
       cluster_sync_all();
@@ -275,6 +303,21 @@ __global__ void __launch_bounds__(640, 1)
             lk = min(max(a.cu_k[s + 1], k0), a.total_k) - k0;
             tiles = (lq + per - 1) / per;
           }
+          // longest first within the 32: lane i takes the sequence of rank i
+          int rank_of = 0;
+#pragma unroll 4
+          for (int o = 1; o < 32; ++o) {
+            const int other = __shfl_sync(0xffffffffu, lk, (lane + o) & 31);
+            rank_of += other > lk || (other == lk && ((lane + o) & 31) < lane);
+          }
+          volatile int* sorted = reinterpret_cast<volatile int*>(smem + C::OFF_SORT);
+          sorted[rank_of] = lane;
+          __syncwarp();
+          const int from = sorted[lane];
+          __syncwarp();
+          q0 = __shfl_sync(0xffffffffu, q0, from), lq = __shfl_sync(0xffffffffu, lq, from);
+          k0 = __shfl_sync(0xffffffffu, k0, from), lk = __shfl_sync(0xffffffffu, lk, from);
+          tiles = __shfl_sync(0xffffffffu, tiles, from);
           incl = tiles;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -647,10 +690,14 @@ __global__ void __launch_bounds__(640, 1)
       } else {
         // Rows go to the CTA that finishes them: CTA r / share keeps rows share * CTA ..; the partial
         // of CTA c, group g is slot 2 c + g: O rows [slot][row][16 n16] float32, then (max, sum) [slot][row].
-        cluster_sync_all();
+        // Few rows: a place of their own that alternates by item, and a barrier that only the warps with rows
+        // meet at; the loads of the next item run on.  (A place is written again two items later, after
+        // the writer passed the next item's barrier, so after every warp finished with this item's rows.)
+        // Many rows: the K / V slots, between two barriers of the whole cluster.
         const int rows = min(f.TQ, it.ntok) * f.G, share = (rows + f.split - 1) / f.split;
         const uint32_t wide = (a.dh + 15) / 16 * 64;  // bytes of a row
-        const uint32_t part = sbase + C::OFF_KV, stats = part + 2 * f.split * share * wide;
+        const uint32_t part = sbase + (f.light ? C::OFF_X + (n & 1) * C::TILE : C::OFF_KV), stats = part + 2 * f.split * share * wide;
+        if (!f.light) cluster_sync_all();
         if (q * 32 < rows) {
           const int owner = min(r / share, f.split - 1), pr = (2 * rank + g) * share + r - owner * share;
           // a row's 16-byte units are rotated by its number: neighbouring rows meet other banks
@@ -674,41 +721,73 @@ __global__ void __launch_bounds__(640, 1)
         __syncwarp();
         if (mine > 0 && elect_one()) mbar_arrive(bar(B::OF + g));
         __syncwarp();
-        cluster_sync_all();
-        // eight columns of one row per thread and step
-        const int units = a.dh / 8, mrows = min(share, rows - rank * share);
-        const uint8_t* gp = smem + C::OFF_KV;
-        const float2* gs = reinterpret_cast<const float2*>(gp + 2 * f.split * share * wide);
-#pragma unroll 1
-        for (int i = threadIdx.x - 128; i < mrows * units; i += 512) {
-          const int lr = i / units, u = i - lr * units, row = rank * share + lr, t = row / f.G, hd = it.hk * f.G + row - t * f.G;
-          float mx = -INFINITY;
-          for (int p = 0; p < 2 * f.split; ++p) mx = fmaxf(mx, gs[p * share + lr].x);
-          float sum = 0.f, o[8] = {};
-          for (int p = 0; p < 2 * f.split; ++p) {
-            const float2 st = gs[p * share + lr];
-            if (st.x == -INFINITY) continue;  // nothing seen: its O row was not written
-            const float w = ex2_approx(st.x - mx);
-            sum += w * st.y;
-            const uint32_t pr = p * share + lr, turn = (pr * 16) % wide;
-            uint32_t a0 = u * 32 + turn, a1 = a0 + 16;
-            if (a0 >= wide) a0 -= wide;
-            if (a1 >= wide) a1 -= wide;
-            const float4 x = *reinterpret_cast<const float4*>(gp + pr * wide + a0), y = *reinterpret_cast<const float4*>(gp + pr * wide + a1);
-            o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
-            o[4] += w * y.x, o[5] += w * y.y, o[6] += w * y.z, o[7] += w * y.w;
+        if (f.light) {
+          if (q == 0) {
+            fence_cluster();
+            __syncwarp();
+            if (lane < f.split) mbar_arrive_cluster(mapa_shared(bar(B::XF + (n & 1)), lane));
+            __syncwarp();
+            ok = mbar_wait_cluster(bar(B::XF + (n & 1)), (n >> 1) & 1, a.status) && ok;
+            __syncwarp();
           }
-          const bool any = mx != -INFINITY;
-          const float inv = any ? 1.0f / sum : 0.f;
-          T* out = static_cast<T*>(a.o) + (it.tok0 + t) * a.o_tok + hd * a.o_head + 8 * u;
-          *reinterpret_cast<uint4*>(out) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
-                                                      pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
-          if (u == 0 && a.lse)
-            a.lse[static_cast<long long>(hd) * a.total_q + it.tok0 + t] = any ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        } else {
+          cluster_sync_all();
         }
-        fence_proxy_async_smem();  // the slots are TMA's again
-        __syncwarp();
-        named_barrier_sync(9, C::THREADS);
+        // a half-warp per row, eight columns per lane
+        const int mrows = min(share, rows - rank * share), u = lane & 15, top = lane & 16;
+        const int step = f.light ? 8 : 32;  // rows per turn: 4 or 16 warps
+        const uint32_t slots = 2 * f.split;
+#pragma unroll 1
+        for (int l0 = f.light ? 2 * (2 * g + hf) : 2 * (warp - 4); (!f.light || q == 0) && l0 < mrows; l0 += step) {
+          const int lr = l0 + (lane >> 4);
+          // lane p holds (max, sum) of slot p
+          float2 st = make_float2(-INFINITY, 0.f);
+          if (u < slots && lr < mrows) st = ld_shared_f2(stats + (u * share + lr) * 8);
+          float mx = st.x;
+#pragma unroll
+          for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+          const float w = st.x == -INFINITY ? 0.f : ex2_approx(st.x - mx);
+          float sum = w * st.y;
+#pragma unroll
+          for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          float o[8] = {};
+          uint32_t pr = lr, turn = (lr * 16) % wide;
+          const uint32_t skip = (share * 16) % wide;
+#pragma unroll 2
+          for (uint32_t p = 0; p < slots; ++p) {
+            const float wp = __shfl_sync(0xffffffffu, w, top + p), mp = __shfl_sync(0xffffffffu, st.x, top + p);
+            if (mp != -INFINITY && lr < mrows && 8 * u < a.dh) {  // else nothing seen: its O row was not written
+              uint32_t a0 = u * 32 + turn, a1 = a0 + 16;
+              if (a0 >= wide) a0 -= wide;
+              if (a1 >= wide) a1 -= wide;
+              const uint4 x = ld_shared_v4(part + pr * wide + a0), y = ld_shared_v4(part + pr * wide + a1);
+              o[0] += wp * __uint_as_float(x.x), o[1] += wp * __uint_as_float(x.y);
+              o[2] += wp * __uint_as_float(x.z), o[3] += wp * __uint_as_float(x.w);
+              o[4] += wp * __uint_as_float(y.x), o[5] += wp * __uint_as_float(y.y);
+              o[6] += wp * __uint_as_float(y.z), o[7] += wp * __uint_as_float(y.w);
+            }
+            pr += share;
+            turn += skip;
+            if (turn >= wide) turn -= wide;
+          }
+          if (lr < mrows) {
+            const bool any = mx != -INFINITY;
+            const float inv = any ? 1.0f / sum : 0.f;
+            const int row = rank * share + lr, t = row / f.G, hd = it.hk * f.G + row - t * f.G;
+            if (8 * u < a.dh) {
+              T* out = static_cast<T*>(a.o) + (it.tok0 + t) * a.o_tok + hd * a.o_head + 8 * u;
+              *reinterpret_cast<uint4*>(out) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                                                          pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+            }
+            if (u == 0 && a.lse)
+              a.lse[static_cast<long long>(hd) * a.total_q + it.tok0 + t] = any ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          }
+        }
+        if (!f.light) {
+          fence_proxy_async_smem();  // the slots are TMA's again
+          __syncwarp();
+          named_barrier_sync(9, C::THREADS);
+        }
       }
     }
   }
@@ -764,22 +843,35 @@ template <int NA, typename T>
 static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, FaArgs& f, int num_sms,
                                cudaStream_t st) {
   const PackedAttnArgs& a = f.a;
-  // most items there can be: every sequence ends inside a tile
-  auto items = [&](long long per) {
-    const long long by_len = (static_cast<long long>(a.max_q) + per - 1) / per * a.n_seq;
-    const long long by_total = a.total_q / per + a.n_seq;
-    return (by_len > 0 && by_len < by_total ? by_len : by_total) * a.Hk;
-  };
-  const long long pairs = items(2 * f.TQ), singles = items(f.TQ);
-  const int nt = (a.max_k + 127) / 128;
-  // One query tile per sequence, or fewer pairs than half the SMs: the split form
-  if (a.max_q > f.TQ && pairs * 2 > num_sms) {
-    return launch_fa<NA, T, false>(tq, tk, tv, f, static_cast<int>(pairs < num_sms ? pairs : num_sms), st);
+  // Form and slices, by what was measured in cycles: a key tile step 2600 (either form: two query tiles, or
+  // two key tiles of one), a pair item 5000 besides, a split item 8000; the longest item, or all items over
+  // the places where they run, whichever lasts longer.  Lengths beyond the longest are averages:
+  // the totals are known here, the offsets are not.
+  auto tiles = [](long long n, long long per) { return (n + per - 1) / per; };
+  const long long avg_q = a.total_q / a.n_seq, avg_k = a.total_k / a.n_seq;
+  auto items = [&](long long per) { return a.n_seq * tiles(avg_q > 0 ? avg_q : 1, per) * a.Hk; };
+  const long long nt_max = tiles(a.max_k, 128), nt_avg = tiles(avg_k, 128);
+  const long long pair_all = items(2 * f.TQ) * (nt_avg * 2600 + 5000) / num_sms;
+  long long best = f.light ? -1 : nt_max * 2600 + 5000 > pair_all ? nt_max * 2600 + 5000 : pair_all;
+  int split = 0;  // the pair form
+  for (int c = 1; c <= 8; c *= 2) {
+    long long cost = tiles(nt_max, 2 * c) * 2600 + 8000;
+    const long long all = items(f.TQ) * (tiles(nt_avg, 2 * c) * 2600 + 8000) / (num_sms / c);
+    if (all > cost) cost = all;
+    if (best < 0 || cost < best) {
+      best = cost;
+      split = c;
+    }
   }
-  f.split = 1;
-  while (f.split < 8 && singles * f.split * 2 <= num_sms && nt >= 4 * f.split) f.split *= 2;
-  const long long clusters = singles < num_sms / f.split ? singles : num_sms / f.split;
-  return launch_fa<NA, T, true>(tq, tk, tv, f, static_cast<int>(clusters) * f.split, st);
+  // items there can be at most: every sequence ends inside a tile
+  auto most = [&](long long per) { return (a.total_q / per + a.n_seq) * a.Hk; };
+  if (split == 0) {
+    const long long n = most(2 * f.TQ);
+    return launch_fa<NA, T, false>(tq, tk, tv, f, static_cast<int>(n < num_sms ? n : num_sms), st);
+  }
+  f.split = split;
+  const long long n = most(f.TQ), places = num_sms / split;
+  return launch_fa<NA, T, true>(tq, tk, tv, f, static_cast<int>(n < places ? n : places) * split, st);
 }
 
 template <typename T>
@@ -787,7 +879,9 @@ static cudaError_t launch_t(const PackedAttnArgs& a, int num_sms, cudaStream_t s
   FaArgs f;
   f.a = a;
   f.G = a.H / a.Hk;
-  f.TQ = 128 / f.G;
+  // few rows per sequence (single tokens): small tiles, whose partial rows are exchanged lightly
+  f.light = f.G <= FaCfg<1, true>::LIGHT_ROWS && a.max_q <= FaCfg<1, true>::LIGHT_ROWS / f.G;
+  f.TQ = (f.light ? FaCfg<1, true>::LIGHT_ROWS : 128) / f.G;
   f.split = 1;
   f.sc = a.scale * 1.4426950408889634f;
   const int dt = a.fp16 ? DIT_DTYPE_FP16 : DIT_DTYPE_BF16;

@@ -52,12 +52,6 @@ __device__ __forceinline__ void add_bias(const LinearArgs& a, int n, float* v) {
   }
 }
 
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-
 // ------------------------------------------------------------------------- SM pairs
 template <int BN, bool F32>
 struct PairCfg {
