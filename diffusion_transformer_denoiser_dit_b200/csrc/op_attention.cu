@@ -284,13 +284,15 @@ __global__ void __launch_bounds__(640, 1)
       if (!ok) after_timeout();
     } else if (warp == 3) {  // ---------------- items
       const int per = C::QT * f.TQ;                       // query tokens per item
-      const long long step = SPLIT ? gridDim.x / f.split : gridDim.x;
-      long long id = SPLIT ? blockIdx.x / f.split : blockIdx.x;
+      // Items are dealt out in rounds, every other one in reverse, so that who got a long one gets a short
+      // one next (sequences are taken longest first).
+      const unsigned step = SPLIT ? gridDim.x / f.split : gridDim.x, place = SPLIT ? blockIdx.x / f.split : blockIdx.x;
       int sb = -32;                                        // sequences sb + lane are in registers
-      long long cum = 0;                                   // items (per head) before them
-      int q0 = 0, lq = 0, k0 = 0, lk = 0, tiles = 0, incl = 0, total = 0;
-      for (int n = 0;; ++n, id += step) {
-        const long long t = id / a.Hk;
+      unsigned cum = 0;                                    // items (per head) before them
+      int q0 = 0, lq = 0, k0 = 0, lk = 0, tiles = 0, incl = 0;
+      unsigned total = 0;
+      for (int n = 0;; ++n) {
+        const unsigned id = n & 1 ? (n + 1) * step - 1 - place : n * step + place, t = id / static_cast<unsigned>(a.Hk);
         while (sb < a.n_seq && t >= cum + total) {
           cum += total;
           sb += 32;
@@ -304,7 +306,8 @@ __global__ void __launch_bounds__(640, 1)
             tiles = (lq + per - 1) / per;
           }
           // longest first within the 32: lane i takes the sequence of rank i
-          int rank_of = 0;
+          if (a.n_seq > 1) {
+            int rank_of = 0;
 #pragma unroll 4
           for (int o = 1; o < 32; ++o) {
             const int other = __shfl_sync(0xffffffffu, lk, (lane + o) & 31);
@@ -318,6 +321,7 @@ __global__ void __launch_bounds__(640, 1)
           q0 = __shfl_sync(0xffffffffu, q0, from), lq = __shfl_sync(0xffffffffu, lq, from);
           k0 = __shfl_sync(0xffffffffu, k0, from), lk = __shfl_sync(0xffffffffu, lk, from);
           tiles = __shfl_sync(0xffffffffu, tiles, from);
+          }
           incl = tiles;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -339,16 +343,16 @@ __global__ void __launch_bounds__(640, 1)
           e.k0 = __shfl_sync(0xffffffffu, k0, src);
           e.nk = Lk;
           e.off = tile * per + Lk - Lq;
-          e.hk = static_cast<int>(id - t * a.Hk);
+          e.hk = static_cast<int>(id - t * static_cast<unsigned>(a.Hk));
           // key tiles that query tokens up to the item's last-th see
           auto seen = [&](int last) {
             const int keys = a.causal ? min(Lk, e.off + last + 1) : Lk;
             return keys > 0 ? (keys + 127) / 128 : 0;
           };
           if constexpr (SPLIT) {
-            const long long nt = seen(e.ntok - 1);
-            e.t0 = static_cast<int>(nt * rank / f.split);
-            e.t1 = static_cast<int>(nt * (rank + 1) / f.split);
+            const int nt = seen(e.ntok - 1);  // at most 2^24
+            e.t0 = nt * rank / f.split;
+            e.t1 = nt * (rank + 1) / f.split;
           } else {
             e.t0 = seen(min(e.ntok, f.TQ) - 1);
             e.t1 = e.ntok > f.TQ ? seen(e.ntok - 1) : 0;
@@ -863,8 +867,10 @@ static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, con
       split = c;
     }
   }
-  // items there can be at most: every sequence ends inside a tile
+  // items there can be at most: every sequence ends inside a tile.  Their numbers, a round beyond the last
+  // among them, are 32-bit in the kernel.
   auto most = [&](long long per) { return (a.total_q / per + a.n_seq) * a.Hk; };
+  if (most(f.TQ) > 0x7fff0000ll) return cudaErrorInvalidValue;
   if (split == 0) {
     const long long n = most(2 * f.TQ);
     return launch_fa<NA, T, false>(tq, tk, tv, f, static_cast<int>(n < num_sms ? n : num_sms), st);
