@@ -95,8 +95,7 @@ dit_status dit_op_attention_packed(int dtype, const void* q, const void* k, cons
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
       !aligned(cu_q, 4) || !aligned(cu_k, 4) || !distinct(total_q, strides[6], heads, strides[7], dh))
     return DIT_ERR_INVALID_ARG;
-  const int sms = current_sms();
-  if (sms == 0) return DIT_ERR_NO_DEVICE;
+  if (current_sms() == 0) return DIT_ERR_NO_DEVICE;
   PackedAttnArgs a;
   a.q = q;
   a.k = k;
@@ -125,7 +124,7 @@ dit_status dit_op_attention_packed(int dtype, const void* q, const void* k, cons
   a.causal = causal != 0;
   a.fp16 = dtype == DIT_DTYPE_FP16;
   a.status = status;
-  return launched(launch_attention_packed(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(launch_attention_packed(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 dit_status dit_rotary_frequencies(int scaling, int pairs, double base, double factor, int original_length, double* freq,

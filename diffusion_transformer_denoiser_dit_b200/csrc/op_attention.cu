@@ -805,15 +805,16 @@ __global__ void __launch_bounds__(640, 1)
   }
 }
 
+// One-time set-up on the current device, and how many clusters of 1, 2, 4 and 8 CTAs run at one time (those
+// of 4 and 8 do not reach every SM; a persistent cluster that has to wait for another would double the time).
 template <int NA, typename T, bool SPLIT>
-static cudaError_t launch_fa(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FaArgs& f, int ctas,
-                             cudaStream_t st) {
+static cudaError_t set_up_fa(int (&places)[4]) {
   using C = FaCfg<NA, SPLIT>;
   auto kernel = attention_tc_kernel<NA, T, SPLIT>;
-  static bool set[kMaxDevices] = {};
+  static int of[kMaxDevices][4] = {};
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
-  if (!set[dev]) {
+  if (of[dev][0] == 0) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     // the register split (setmaxnreg) must fit in the launch allocation, or it would wait forever
@@ -821,8 +822,32 @@ static cudaError_t launch_fa(const CUtensorMap& tq, const CUtensorMap& tk, const
     e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return e;
     if (fa.numRegs * C::THREADS < C::REG_POOL) return cudaErrorInvalidConfiguration;
-    set[dev] = true;
+    for (int i = 3; i >= 0; --i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(1184);
+      cfg.blockDim = dim3(C::THREADS);
+      cfg.dynamicSmemBytes = C::SMEM;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim = {1u << i, 1, 1};
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n <= 0) return cudaErrorInvalidConfiguration;
+      of[dev][i] = n;
+    }
   }
+  for (int i = 0; i < 4; ++i) places[i] = of[dev][i];
+  return cudaSuccess;
+}
+
+template <int NA, typename T, bool SPLIT>
+static cudaError_t launch_fa(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const FaArgs& f, int ctas,
+                             cudaStream_t st) {
+  using C = FaCfg<NA, SPLIT>;
+  auto kernel = attention_tc_kernel<NA, T, SPLIT>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(C::THREADS);
@@ -844,7 +869,7 @@ static cudaError_t launch_fa(const CUtensorMap& tq, const CUtensorMap& tk, const
 }
 
 template <int NA, typename T>
-static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, FaArgs& f, int num_sms,
+static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, FaArgs& f,
                                cudaStream_t st) {
   const PackedAttnArgs& a = f.a;
   // Form and slices, by what was measured in cycles: a key tile step 2600 (either form: two query tiles, or
@@ -855,12 +880,15 @@ static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, con
   const long long avg_q = a.total_q / a.n_seq, avg_k = a.total_k / a.n_seq;
   auto items = [&](long long per) { return a.n_seq * tiles(avg_q > 0 ? avg_q : 1, per) * a.Hk; };
   const long long nt_max = tiles(a.max_k, 128), nt_avg = tiles(avg_k, 128);
-  const long long pair_all = items(2 * f.TQ) * (nt_avg * 2600 + 5000) / num_sms;
+  int places[4];
+  cudaError_t e = set_up_fa<NA, T, true>(places);
+  if (e != cudaSuccess) return e;
+  const long long pair_all = items(2 * f.TQ) * (nt_avg * 2600 + 5000) / places[0];
   long long best = f.light ? -1 : nt_max * 2600 + 5000 > pair_all ? nt_max * 2600 + 5000 : pair_all;
   int split = 0;  // the pair form
-  for (int c = 1; c <= 8; c *= 2) {
+  for (int i = 0, c = 1; i < 4; ++i, c *= 2) {
     long long cost = tiles(nt_max, 2 * c) * 2600 + 8000;
-    const long long all = items(f.TQ) * (tiles(nt_avg, 2 * c) * 2600 + 8000) / (num_sms / c);
+    const long long all = items(f.TQ) * (tiles(nt_avg, 2 * c) * 2600 + 8000) / places[i];
     if (all > cost) cost = all;
     if (best < 0 || cost < best) {
       best = cost;
@@ -872,16 +900,19 @@ static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, con
   auto most = [&](long long per) { return (a.total_q / per + a.n_seq) * a.Hk; };
   if (most(f.TQ) > 0x7fff0000ll) return cudaErrorInvalidValue;
   if (split == 0) {
+    e = set_up_fa<NA, T, false>(places);
+    if (e != cudaSuccess) return e;
     const long long n = most(2 * f.TQ);
-    return launch_fa<NA, T, false>(tq, tk, tv, f, static_cast<int>(n < num_sms ? n : num_sms), st);
+    return launch_fa<NA, T, false>(tq, tk, tv, f, static_cast<int>(n < places[0] ? n : places[0]), st);
   }
   f.split = split;
-  const long long n = most(f.TQ), places = num_sms / split;
-  return launch_fa<NA, T, true>(tq, tk, tv, f, static_cast<int>(n < places ? n : places) * split, st);
+  const int fit = places[split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3];
+  const long long n = most(f.TQ);
+  return launch_fa<NA, T, true>(tq, tk, tv, f, static_cast<int>(n < fit ? n : fit) * split, st);
 }
 
 template <typename T>
-static cudaError_t launch_t(const PackedAttnArgs& a, int num_sms, cudaStream_t st) {
+static cudaError_t launch_t(const PackedAttnArgs& a, cudaStream_t st) {
   FaArgs f;
   f.a = a;
   f.G = a.H / a.Hk;
@@ -908,11 +939,11 @@ static cudaError_t launch_t(const PackedAttnArgs& a, int num_sms, cudaStream_t s
              !map(&tv, a.v, a.Hk, a.total_k, a.v_head, a.v_tok, 1, 128)) {
     return cudaErrorInvalidValue;
   }
-  return a.dh <= 64 ? launch_form<1, T>(tq, tk, tv, f, num_sms, st) : launch_form<2, T>(tq, tk, tv, f, num_sms, st);
+  return a.dh <= 64 ? launch_form<1, T>(tq, tk, tv, f, st) : launch_form<2, T>(tq, tk, tv, f, st);
 }
 
-cudaError_t launch_attention_packed(const PackedAttnArgs& a, int num_sms, cudaStream_t st) {
-  return a.fp16 ? launch_t<__half>(a, num_sms, st) : launch_t<__nv_bfloat16>(a, num_sms, st);
+cudaError_t launch_attention_packed(const PackedAttnArgs& a, cudaStream_t st) {
+  return a.fp16 ? launch_t<__half>(a, st) : launch_t<__nv_bfloat16>(a, st);
 }
 
 }  // namespace dit

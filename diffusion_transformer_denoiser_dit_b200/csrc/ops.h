@@ -41,7 +41,7 @@ struct PackedAttnArgs {
   int causal, fp16;
   int* status;
 };
-cudaError_t launch_attention_packed(const PackedAttnArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_attention_packed(const PackedAttnArgs& a, cudaStream_t st);
 
 struct RotaryArgs {
   const void *x, *pos;
