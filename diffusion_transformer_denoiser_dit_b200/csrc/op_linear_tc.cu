@@ -458,41 +458,49 @@ struct SplitCfg {
   }
 };
 
-// 128 bytes (64 values) of `rows` rows from p (row r0, column k0) into a 128-byte-swizzled tile,
-// by 128 threads; values outside [R, K] are zero
+// 128 bytes (64 values) of `rows` rows from p (row r0, column k0) into a 128-byte-swizzled tile, by 128
+// threads; values outside [R, K] are zero.  Rows aligned to 4 or 8 bytes are copied asynchronously
+// (cp.async of that many bytes, the caller waits for its group), others through registers.
 template <typename T>
-__device__ __forceinline__ void gather_tile(uint8_t* dst, const T* p, long long ld, int r0, int R, int k0, int K, int rows,
+__device__ __forceinline__ void gather_tile(uint32_t dst, const T* p, long long ld, int r0, int R, int k0, int K, int rows,
                                             int grain, int tid) {
-  for (int i0 = tid; i0 < rows * 8; i0 += 128 * 4) {
-    uint32_t v[4][4];
+  if (grain >= 4) {
+    const int per_row = 128 / grain, vals = grain / 2;
+    const int c = tid % per_row, k = k0 + c * vals;  // a thread keeps its columns
+    const uint32_t at = static_cast<uint32_t>(c * grain);
+    const int in_row = min(max(K - k, 0), vals) * 2;
+    const T* src = p + k;
+#pragma unroll 4
+    for (int r = tid / per_row; r < rows; r += 128 / per_row) {
+      const uint32_t to = dst + r * 128 + ((at & 112u) ^ ((r & 7) << 4)) + (at & 15u);
+      const int bytes = r0 + r < R ? in_row : 0;
+      const T* from = bytes > 0 ? src + (r0 + r) * ld : p;  // nothing is read of it where bytes is 0
+      if (grain == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    }
+    return;
+  }
+  for (int i0 = tid; i0 < rows * 8; i0 += 128 * 2) {
+    uint32_t v[2][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const int i = i0 + j * 128, r = i >> 3, k = k0 + (i & 7) * 8;
       v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
-      if (i >= rows * 8 || r0 + r >= R || k >= K) continue;
-      const T* src = p + (r0 + r) * ld + k;
-      if (grain == 8 && k + 8 <= K) {
-        const uint2 a = *reinterpret_cast<const uint2*>(src), b = *reinterpret_cast<const uint2*>(src + 4);
-        v[j][0] = a.x, v[j][1] = a.y, v[j][2] = b.x, v[j][3] = b.y;
-      } else if (grain >= 4 && k + 8 <= K) {
+      if (i >= rows * 8 || r0 + r >= R) continue;
+      const uint16_t* s = reinterpret_cast<const uint16_t*>(p + (r0 + r) * ld + k);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[j][e] = reinterpret_cast<const uint32_t*>(src)[e];
-      } else {
-        const uint16_t* s = reinterpret_cast<const uint16_t*>(src);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (k + e < K) v[j][e >> 1] |= static_cast<uint32_t>(s[e]) << (16 * (e & 1));
-      }
+      for (int e = 0; e < 8; ++e)
+        if (k + e < K) v[j][e >> 1] |= static_cast<uint32_t>(s[e]) << (16 * (e & 1));
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const int i = i0 + j * 128, r = i >> 3, u = i & 7;
-      if (i < rows * 8)
-        *reinterpret_cast<uint4*>(dst + r * 128 + ((u ^ (r & 7)) << 4)) = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
+      if (i < rows * 8) st_shared_v4(dst + r * 128 + ((u ^ (r & 7)) << 4), v[j][0], v[j][1], v[j][2], v[j][3]);
     }
   }
 }
-
 
 struct SplitArgs {
   int split;            // CTAs per cluster: K slices of a tile
@@ -526,6 +534,7 @@ __global__ void __launch_bounds__(192)
   // rows of the tile that one CTA of the cluster finishes
   const int share = (min(128, a.M - m0) + sp.split - 1) / sp.split;
   const int gathered = GATHER ? (sp.grain_x != 0) + (sp.grain_w != 0) : 0;
+  const int gather_rows = min(128, (a.M - m0 + 7) & ~7);  // the rest of the tile only reaches rows past M
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -609,21 +618,36 @@ __global__ void __launch_bounds__(192)
   } else {  // ------------------------ warps 2..5: gather, then one row of sums per thread
     const int tid = threadIdx.x - 64, q = warp & 3, r = q * 32 + lane;
     if (GATHER && gathered > 0) {
-      int s = 0;
+      // copies of up to AHEAD stages are in flight; a stage is handed over when this thread's share landed
+      constexpr int AHEAD = 3;
+      static_assert(C::STAGES > AHEAD, "stages");
+      int s = 0, full = 0;
       uint32_t ph = 0;
-      for (int kb = kb_begin; kb < kb_end; ++kb) {
-        if (!mbar_wait_spin(EMPTY(s), ph ^ 1u, a.status)) break;
-        uint8_t* sa = smem + s * C::STAGE;
-        if (sp.grain_x) gather_tile(sa, static_cast<const T*>(a.x), a.ldx, m0, a.M, kb * 64, a.K, 128, sp.grain_x, tid);
-        if (sp.grain_w)
-          gather_tile(sa + C::A_BYTES, static_cast<const T*>(a.w), a.ldw, n0, a.N, kb * 64, a.K, BN, sp.grain_w, tid);
-        fence_proxy_async_smem();
-        mbar_arrive(FULL(s));
-        if (++s == C::STAGES) {
-          s = 0;
-          ph ^= 1u;
+      bool ok = true;
+      for (int kb = kb_begin; kb < kb_end + AHEAD; ++kb) {
+        if (kb < kb_end) {
+          ok = ok && mbar_wait_spin(EMPTY(s), ph ^ 1u, a.status);
+          if (ok) {
+            const uint32_t sa = sbase + s * C::STAGE;
+            if (sp.grain_x)
+              gather_tile(sa, static_cast<const T*>(a.x), a.ldx, m0, a.M, kb * 64, a.K, gather_rows, sp.grain_x, tid);
+            if (sp.grain_w)
+              gather_tile(sa + C::A_BYTES, static_cast<const T*>(a.w), a.ldw, n0, a.N, kb * 64, a.K, BN, sp.grain_w, tid);
+          }
+          if (++s == C::STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (kb - AHEAD >= kb_begin) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
+          fence_proxy_async_smem();
+          if (ok) mbar_arrive(FULL(full));
+          if (++full == C::STAGES) full = 0;
         }
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncwarp();
     }
     // Row r goes to the CTA that finishes it: CTA r / share keeps rows share * CTA .. of the tile,
@@ -811,12 +835,13 @@ static cudaError_t launch_tc(const LinearArgs& a, int num_sms, cudaStream_t st) 
   const int rows = a.M >= 128 ? 128 : a.M;
   int fit[4];
   if (!split_clusters<T>(fit)) return cudaErrorInvalidConfiguration;
+  const bool gather = !(map_rows(&tx, dt, a.x, a.M, a.K, a.ldx, 8, 64) && map_rows(&tw, dt, a.w, a.N, a.K, a.ldw, 64, 64));
   bool narrow = false;
   long long best = -1;
   for (int bn = 128; bn >= 64; bn -= 64)
     for (int i = 0, split = 1; i < 4 && 2 * split <= kblocks + 1; ++i, split *= 2) {
       const long long rounds = (mt * ((a.N + bn - 1) / bn) + fit[i] - 1) / fit[i];
-      const long long cost = rounds * (5300 + (kblocks + split - 1) / split * 370 + (bn == 64 ? 3600 : 7600) * rows / 128);
+      const long long cost = rounds * (5300 + (kblocks + split - 1) / split * (gather ? 900 : 370) + (bn == 64 ? 3600 : 7600) * rows / 128);
       if (best < 0 || cost < best) {
         best = cost;
         sp.split = split;
@@ -835,7 +860,6 @@ static cudaError_t launch_tc(const LinearArgs& a, int num_sms, cudaStream_t st) 
   if (sp.grain_x && sp.grain_w) tx = tw = CUtensorMap{};
   else if (sp.grain_x) tx = tw;
   else if (sp.grain_w) tw = tx;
-  const bool gather = sp.grain_x || sp.grain_w;
   if (narrow)
     return gather ? launch_split<64, T, true>(a, tx, tw, sp, box_rows, st)
                   : launch_split<64, T, false>(a, tx, tw, sp, box_rows, st);
