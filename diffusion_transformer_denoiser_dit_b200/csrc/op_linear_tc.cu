@@ -458,28 +458,46 @@ struct SplitCfg {
   }
 };
 
+// `rows` rows (a multiple of 8) of 128 bytes into a 128-byte-swizzled tile by 128 threads, GRAIN bytes (4 or
+// 8) per cp.async: this thread's column of them, `bytes` of it inside the matrix, rows row0, row0 + GRAIN, ..;
+// rows from `real` on are zeros.  Addresses advance by additions (with the row times the stride formed
+// anew for each, an iteration took 166 cycles).
+template <int GRAIN>
+__device__ __forceinline__ void gather_async(uint32_t dst, const uint8_t* src, long long ld_bytes, int row0, int rows,
+                                             int real, int col_bytes, int bytes) {
+#pragma unroll
+  for (int sub = 0; sub < 8 / GRAIN; ++sub) {  // the row modulo 8, and so the swizzle, stays in this loop
+    const int r = row0 + sub * GRAIN;
+    uint32_t to = dst + r * 128 + ((col_bytes & 112) ^ ((r & 7) << 4)) + (col_bytes & 15);
+    const uint8_t* from = src + r * ld_bytes;
+    const long long step = 8 * ld_bytes;
+    int left = (real - r + 7) >> 3;           // rows of this thread inside the matrix
+    if (left <= 0) from = src;
+#pragma unroll 4
+    for (int i = r; i < rows; i += 8) {
+      const int n = left > 0 ? bytes : 0;
+      if constexpr (GRAIN == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+      to += 1024;
+      if (--left > 0) from += step;           // never past the last row
+    }
+  }
+}
+
 // 128 bytes (64 values) of `rows` rows from p (row r0, column k0) into a 128-byte-swizzled tile, by 128
-// threads; values outside [R, K] are zero.  Rows aligned to 4 or 8 bytes are copied asynchronously
-// (cp.async of that many bytes, the caller waits for its group), others through registers.
+// threads; values outside [R, K] are zero.  Rows aligned to 4 or 8 bytes are copied asynchronously (the
+// caller waits for its group), others through registers.
 template <typename T>
 __device__ __forceinline__ void gather_tile(uint32_t dst, const T* p, long long ld, int r0, int R, int k0, int K, int rows,
                                             int grain, int tid) {
   if (grain >= 4) {
-    const int per_row = 128 / grain, vals = grain / 2;
-    const int c = tid % per_row, k = k0 + c * vals;  // a thread keeps its columns
-    const uint32_t at = static_cast<uint32_t>(c * grain);
-    const int in_row = min(max(K - k, 0), vals) * 2;
-    const T* src = p + k;
-#pragma unroll 4
-    for (int r = tid / per_row; r < rows; r += 128 / per_row) {
-      const uint32_t to = dst + r * 128 + ((at & 112u) ^ ((r & 7) << 4)) + (at & 15u);
-      const int bytes = r0 + r < R ? in_row : 0;
-      const T* from = bytes > 0 ? src + (r0 + r) * ld : p;  // nothing is read of it where bytes is 0
-      if (grain == 8)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-      else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-    }
+    const int c = grain == 8 ? tid & 15 : tid & 31, row0 = grain == 8 ? tid >> 4 : tid >> 5, k = k0 + c * (grain >> 1);
+    const int bytes = min(max(K - k, 0) * 2, grain);
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(p + r0 * ld + (k < K ? k : 0));
+    if (grain == 8) gather_async<8>(dst, src, ld * 2, row0, rows, R - r0, c * 8, bytes);
+    else gather_async<4>(dst, src, ld * 2, row0, rows, R - r0, c * 4, bytes);
     return;
   }
   for (int i0 = tid; i0 < rows * 8; i0 += 128 * 2) {
@@ -683,66 +701,84 @@ __global__ void __launch_bounds__(192)
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM);
   }
-  // this CTA's rows: a thread keeps its four columns and steps through the rows, slices added in
-  // their order
-  constexpr int UNITS = BN / 4, STEP = 192 / UNITS;
+  // this CTA's rows: a thread keeps its four columns and steps through the rows, slices added in their order;
+  // four rows at a time, whose residuals are on their way together
+  constexpr int UNITS = BN / 4, STEP = 192 / UNITS, BATCH = 4;
   static_assert(192 % UNITS == 0, "whole rows per step");
   const int u = threadIdx.x % UNITS, n = n0 + 4 * u, r0 = m0 + rank * share, rows = min(share, a.M - r0);
   if (n >= a.N) return;
   const bool vec = sp.vec && n + 4 <= a.N;
   const int cols = min(4, a.N - n);
+  float bias[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) bias[e] = a.bias && e < cols ? __ldg(a.bias + n + e) : 0.f;
+  with_act(a.act, [&](auto act) {
 #pragma unroll 1
-  for (int r = threadIdx.x / UNITS; r < rows; r += STEP) {
-    float v[4], res[4] = {};
-    const long long ar = (r0 + r) * a.ldr + n, ay = (r0 + r) * a.ldy + n;
-    if (a.residual) {
-      if (a.out_f32) {
-        const float* p = static_cast<const float*>(a.residual) + ar;
-        if (vec) *reinterpret_cast<float4*>(res) = *reinterpret_cast<const float4*>(p);
-        else
+    for (int r = threadIdx.x / UNITS; r < rows; r += BATCH * STEP) {
+      float v[BATCH][4], res[BATCH][4];
+      if (a.residual) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) res[e] = e < cols ? p[e] : 0.f;
+        for (int k = 0; k < BATCH; ++k) {
+          const long long at = (r0 + min(r + k * STEP, rows - 1)) * a.ldr + n;
+          if (a.out_f32) {
+            const float* p = static_cast<const float*>(a.residual) + at;
+            if (vec) *reinterpret_cast<float4*>(res[k]) = *reinterpret_cast<const float4*>(p);
+            else
+#pragma unroll
+              for (int e = 0; e < 4; ++e) res[k][e] = e < cols ? p[e] : 0.f;
+          } else {
+            const T* p = static_cast<const T*>(a.residual) + at;
+            if (vec) {
+              const uint2 w = *reinterpret_cast<const uint2*>(p);
+              const float2 y0 = unpack2<T>(w.x), y1 = unpack2<T>(w.y);
+              res[k][0] = y0.x, res[k][1] = y0.y, res[k][2] = y1.x, res[k][3] = y1.y;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) res[k][e] = e < cols ? to_f32(p[e]) : 0.f;
+            }
+          }
+        }
       } else {
-        const T* p = static_cast<const T*>(a.residual) + ar;
-        if (vec) {
-          const uint2 w = *reinterpret_cast<const uint2*>(p);
-          const float2 y0 = unpack2<T>(w.x), y1 = unpack2<T>(w.y);
-          res[0] = y0.x, res[1] = y0.y, res[2] = y1.x, res[3] = y1.y;
-        } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) res[e] = e < cols ? to_f32(p[e]) : 0.f;
+        for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) res[k][e] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = bias[e];
+      for (int j = 0; j < sp.split; ++j)
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+          const uint4 p = ld_shared_v4(part + C::part_at(j * share + min(r + k * STEP, rows - 1), u));
+          v[k][0] += __uint_as_float(p.x), v[k][1] += __uint_as_float(p.y);
+          v[k][2] += __uint_as_float(p.z), v[k][3] += __uint_as_float(p.w);
+        }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        if (r + k * STEP >= rows) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = activate<decltype(act)::value>(v[k][e]) + res[k][e];
+        const long long at = (r0 + r + k * STEP) * a.ldy + n;
+        if (a.out_f32) {
+          float* p = static_cast<float*>(a.y) + at;
+          if (vec) *reinterpret_cast<float4*>(p) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
+          else
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e < cols) p[e] = v[k][e];
+        } else {
+          T* p = static_cast<T*>(a.y) + at;
+          if (vec) *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[k][0], v[k][1]), pack2<T>(v[k][2], v[k][3]));
+          else
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e < cols) p[e] = from_f32<T>(v[k][e]);
         }
       }
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = a.bias && e < cols ? __ldg(a.bias + n + e) : 0.f;
-    for (int j = 0; j < sp.split; ++j) {
-      const uint4 p = ld_shared_v4(part + C::part_at(j * share + r, u));
-      v[0] += __uint_as_float(p.x), v[1] += __uint_as_float(p.y);
-      v[2] += __uint_as_float(p.z), v[3] += __uint_as_float(p.w);
-    }
-    with_act(a.act, [&](auto act) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = activate<decltype(act)::value>(v[e]);
-    });
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += res[e];
-    if (a.out_f32) {
-      float* p = static_cast<float*>(a.y) + ay;
-      if (vec) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-      else
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < cols) p[e] = v[e];
-    } else {
-      T* p = static_cast<T*>(a.y) + ay;
-      if (vec) *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
-      else
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < cols) p[e] = from_f32<T>(v[e]);
-    }
-  }
+  });
 }
 
 template <int BN, typename T, bool GATHER>
