@@ -500,23 +500,35 @@ __device__ __forceinline__ void gather_tile(uint32_t dst, const T* p, long long 
     else gather_async<4>(dst, src, ld * 2, row0, rows, R - r0, c * 4, bytes);
     return;
   }
-  for (int i0 = tid; i0 < rows * 8; i0 += 128 * 2) {
-    uint32_t v[2][4];
+  // Odd element offsets: a thread takes 16 bytes of every 16th row from the aligned words around them (a word
+  // that holds a value of the matrix can be read whole) and shifts; four rows in flight.
+  const int u = tid & 7, row0 = tid >> 3, k = k0 + u * 8, n = min(max(K - k, 0), 8);
+  const uintptr_t base = reinterpret_cast<uintptr_t>(p + r0 * ld + k);
+  const long long step = 16 * ld * 2;
+  uintptr_t at = base + row0 * ld * 2;
+  const uint32_t to = dst + row0 * 128 + ((u ^ (row0 & 7)) << 4);
+  for (int i = 0; row0 + i * 16 < rows; i += 4) {
+    uint32_t w[4][5];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = i0 + j * 128, r = i >> 3, k = k0 + (i & 7) * 8;
-      v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
-      if (i >= rows * 8 || r0 + r >= R) continue;
-      const uint16_t* s = reinterpret_cast<const uint16_t*>(p + (r0 + r) * ld + k);
+    for (int j = 0; j < 4; ++j) {
+      const bool in = r0 + row0 + (i + j) * 16 < R && row0 + (i + j) * 16 < rows;
+      const uintptr_t src = at + j * step;
+      const int words = in && n > 0 ? static_cast<int>(((src & 2) + 2 * n + 3) >> 2) : 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (k + e < K) v[j][e >> 1] |= static_cast<uint32_t>(s[e]) << (16 * (e & 1));
+      for (int e = 0; e < 5; ++e) w[j][e] = e < words ? reinterpret_cast<const uint32_t*>(src & ~uintptr_t(3))[e] : 0u;
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = i0 + j * 128, r = i >> 3, u = i & 7;
-      if (i < rows * 8) st_shared_v4(dst + r * 128 + ((u ^ (r & 7)) << 4), v[j][0], v[j][1], v[j][2], v[j][3]);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t shift = static_cast<uint32_t>((at + j * step) & 2) * 8;
+      uint32_t v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = __funnelshift_r(w[j][e], w[j][e + 1], shift);
+        if (n < 2 * e + 2) v[e] = n == 2 * e + 1 ? v[e] & 0xffffu : 0u;  // values past K
+      }
+      if (row0 + (i + j) * 16 < rows) st_shared_v4(to + (i + j) * 16 * 128, v[0], v[1], v[2], v[3]);
     }
+    at += 4 * step;
   }
 }
 
