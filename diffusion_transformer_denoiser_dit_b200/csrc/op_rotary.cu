@@ -15,19 +15,18 @@
 
 namespace dit {
 
-constexpr int kRotaryThreads = 256;
+constexpr int kRotaryThreads = 128;
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
   T v[V];
 };
 
-// PAIR items: V pairs of one (token, head), two vectors of V elements each; REST items: V
-// elements behind the rotated part, copied.
+// V pairs of a row at a time, two vectors of V elements; `rest` vectors behind the turned part.
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRotaryThreads)
+__global__ void __launch_bounds__(kRotaryThreads, 10)
     rotary_kernel(const __grid_constant__ dit_rotary r, const RotaryArgs a, const int TT, const int rest) {
-  extern __shared__ float2 cs[];  // [TT][P] (cos, sin) times the amplitude
+  extern __shared__ float2 cs[];  // [TT][V][P / V] (cos, sin) times the amplitude
   const int P = r.pairs, each = P / r.axes;
   const int t0 = blockIdx.x * TT, nt = min(TT, a.tokens - t0);
   pdl_trigger();
@@ -39,35 +38,48 @@ __global__ void __launch_bounds__(kRotaryThreads)
     const uint64_t turn = static_cast<uint64_t>(pos) * r.turns[k - axis * each];
     float s, c;
     sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
-    cs[i] = make_float2(c * r.amplitude, (a.transpose ? -s : s) * r.amplitude);
+    // pair k = V c + j of a token at [j][c]: the lanes of a row read neighbouring entries
+    cs[t * P + (k % V) * (P / V) + k / V] = make_float2(c * r.amplitude, (a.transpose ? -s : s) * r.amplitude);
   }
   __syncthreads();
-  const int pc = P / V, per = pc + rest;  // items per (token, head)
-  const int items = nt * a.heads * per;
-  for (int i = threadIdx.x; i < items; i += kRotaryThreads) {
-    const int th = i / per, c = i - th * per, t = th / a.heads, h = th - t * a.heads;
-    const T* x = static_cast<const T*>(a.x) + (t0 + t) * a.x_tok + h * a.x_head;
-    T* y = static_cast<T*>(a.y) + (t0 + t) * a.y_tok + h * a.y_head;
-    if (c >= pc) {
-      const int e = 2 * P + (c - pc) * V;
-      *reinterpret_cast<Vec<T, V>*>(y + e) = *reinterpret_cast<const Vec<T, V>*>(x + e);
-      continue;
-    }
+  // A thread keeps its pairs c of a row (one head of one token) and steps through the rows of the block's
+  // tokens; it also copies every pc-th vector behind the turned part.  One row at a time in small blocks:
+  // ten blocks of an SM overlap their loads (32768 x 20 x 128 bf16, half turned: 55 us, 6.1 TB/s; all
+  // turned: 61 us, with four rows in flight per thread and three blocks of 256: 123 us).
+  const int pc = P / V;
+  for (int c0 = 0; c0 < pc; c0 += kRotaryThreads) {
+    const int wide = min(pc - c0, kRotaryThreads), together = kRotaryThreads / wide;  // rows at a time
+    const int c = c0 + static_cast<int>(threadIdx.x) % wide, first = static_cast<int>(threadIdx.x) / wide;
+    if (first >= together) continue;
     const int ea = INTERLEAVED ? 2 * V * c : V * c, eb = INTERLEAVED ? ea + V : P + V * c;
-    Vec<T, V> u = *reinterpret_cast<const Vec<T, V>*>(x + ea), w = *reinterpret_cast<const Vec<T, V>*>(x + eb);
-    const float2* f = cs + t * P + c * V;
+    const int rows = nt * a.heads;
+    int t = first / a.heads, h = first - t * a.heads;
+    for (int r = first; r < rows; r += together) {
+      const T* x = static_cast<const T*>(a.x) + (t0 + t) * a.x_tok + h * a.x_head;
+      T* y = static_cast<T*>(a.y) + (t0 + t) * a.y_tok + h * a.y_head;
+      Vec<T, V> u = *reinterpret_cast<const Vec<T, V>*>(x + ea), w = *reinterpret_cast<const Vec<T, V>*>(x + eb);
+      for (int e = c; e < rest; e += 2 * pc) {
+        const bool two = e + pc < rest;
+        Vec<T, V> m = *reinterpret_cast<const Vec<T, V>*>(x + 2 * P + e * V), l;
+        if (two) l = *reinterpret_cast<const Vec<T, V>*>(x + 2 * P + (e + pc) * V);
+        *reinterpret_cast<Vec<T, V>*>(y + 2 * P + e * V) = m;
+        if (two) *reinterpret_cast<Vec<T, V>*>(y + 2 * P + (e + pc) * V) = l;
+      }
+      const float2* f = cs + t * P + c;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      // pair j of this item: (u[j], w[j]), or element 2j of the two vectors back to back
-      T& p = INTERLEAVED ? (2 * j < V ? u.v[(2 * j) % V] : w.v[(2 * j) % V]) : u.v[j];
-      T& q = INTERLEAVED ? (2 * j + 1 < V ? u.v[(2 * j + 1) % V] : w.v[(2 * j + 1) % V]) : w.v[j];
-      const float xa = to_f32(p), xb = to_f32(q);
-      const float2 g = f[j];
-      p = from_f32<T>(xa * g.x - xb * g.y);
-      q = from_f32<T>(xb * g.x + xa * g.y);
+      for (int j = 0; j < V; ++j) {
+        // pair j of this item: (u[j], w[j]), or element 2j of the two vectors back to back
+        T& p = INTERLEAVED ? (2 * j < V ? u.v[(2 * j) % V] : w.v[(2 * j) % V]) : u.v[j];
+        T& q = INTERLEAVED ? (2 * j + 1 < V ? u.v[(2 * j + 1) % V] : w.v[(2 * j + 1) % V]) : w.v[j];
+        const float xa = to_f32(p), xb = to_f32(q);
+        const float2 g = f[j * pc];
+        p = from_f32<T>(xa * g.x - xb * g.y);
+        q = from_f32<T>(xb * g.x + xa * g.y);
+      }
+      *reinterpret_cast<Vec<T, V>*>(y + ea) = u;
+      *reinterpret_cast<Vec<T, V>*>(y + eb) = w;
+      for (h += together; h >= a.heads; h -= a.heads) ++t;
     }
-    *reinterpret_cast<Vec<T, V>*>(y + ea) = u;
-    *reinterpret_cast<Vec<T, V>*>(y + eb) = w;
   }
 }
 
