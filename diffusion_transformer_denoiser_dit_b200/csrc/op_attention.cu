@@ -36,7 +36,7 @@ namespace dit {
 
 // One pair of probabilities in every kPolyEvery is exponentiated by a polynomial on the FMA pipe: the MUFU
 // unit gives 16 exponentials a cycle and SM, as long for a 128 x 128 tile as its two products at dh = 128.
-constexpr int kPolyEvery = 4;
+constexpr int kPolyEvery = 5;
 
 // 2^x of a pair, x clamped to >= -126: x = n + f with n the nearest integer (adding and subtracting
 // 1.5 * 2^23), 2^f by a quartic fitted on [-1/2, 1/2] by reweighted least squares on the relative error (at
@@ -231,8 +231,7 @@ __global__ void __launch_bounds__(640, 1)
     it.tok0 = uniform(s.tok0), it.ntok = uniform(s.ntok), it.k0 = uniform(s.k0), it.nk = uniform(s.nk);
     it.off = uniform(s.off), it.hk = uniform(s.hk), it.t0 = uniform(s.t0), it.t1 = uniform(s.t1);
     __syncwarp();
-    if (elect_one()) mbar_arrive(bar(B::IE + (n & 1)));
-    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(B::IE + (n & 1)));
     return ok && it.ntok >= 0;
   };
   // A wait that ran out: the role does no more work, but keeps step in the exchanges; what it
@@ -414,7 +413,9 @@ __global__ void __launch_bounds__(640, 1)
         }
       };
       auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && mbar_wait_warp(b, parity, a.status); };
-      for (int n = 0; next_item(n, it); ++n) {
+      FaItem nx;  // read while the current item still runs
+      bool more = next_item(0, it);
+      for (int n = 0; more; ++n) {
         const int qb = n % C::QB;
         int mine[2];  // key tiles of each group
         if constexpr (SPLIT) {
@@ -496,6 +497,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
           for (int g = 0; g < 2; ++g)
             if (mine[g] > 0) k_of(g);
+          if (f.light) more = next_item(n + 1, nx);
           for (int j = 0; j < all; ++j) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -519,6 +521,7 @@ __global__ void __launch_bounds__(640, 1)
             release(bar(B::KE + kslot[0]));
             step2(kslot[0], kph[0]);
           }
+          more = next_item(n + 1, nx);
           for (int j = 0; j < all; ++j) {
             const int kat = kslot[0], vat = vslot[0];
             if (j + 1 < all) wait(bar(B::KF + kat), kph[0]);
@@ -542,6 +545,8 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
         for (int g = 0; g < 2; ++g) ni[g] += mine[g] > 0;
         exchange_others();
+        if (SPLIT && !f.light) more = next_item(n + 1, nx);
+        it = nx;
       }
       if (!ok) after_timeout();
     } else {  // ---------------- warp 2 only keeps step
