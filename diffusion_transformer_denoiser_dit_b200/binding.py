@@ -332,6 +332,8 @@ class _Runtime:
     def __init__(self):
         import torch
         self.torch, self.lib = torch, load()
+        self.linear, self.attention, self.rotary = (self.lib.dit_op_linear_fused, self.lib.dit_op_attention_packed,
+                                                    self.lib.dit_op_rotary)
         self.float32, self.int32, self.int64 = torch.float32, torch.int32, torch.int64
         self.code = {torch.float32: DIT_DTYPE_F32, torch.bfloat16: DIT_DTYPE_BF16, torch.float16: DIT_DTYPE_FP16}
         self.code16 = {torch.bfloat16: DIT_DTYPE_BF16, torch.float16: DIT_DTYPE_FP16}
@@ -355,37 +357,36 @@ def _no_dtype(name: str, dtype):
     raise TypeError(f"{name}: dtype {dtype} is not supported")
 
 
-def _enqueue(rt: _Runtime, name: str, fn, tensors, stream, args):
-    """fn(*args, stream) on the tensors' device and stream; raises DitError on a refusal."""
-    dev = tensors[0].get_device()
-    if dev < 0:
-        raise ValueError(f"{name}: needs CUDA tensors")
+def _elsewhere(rt: _Runtime, name: str, fn, dev: int, tensors, stream, args):
+    """fn(*args, stream) off the common path: refuses what is not on one CUDA device, takes a given
+    stream, or enters the tensors' device when another is current."""
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: tensors on {t.device} and {tensors[0].device}")
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError(f"{name}: stream on {stream.device}, tensors on {tensors[0].device}")
+    if dev < 0:
+        raise ValueError(f"{name}: needs CUDA tensors")
+    if stream is None:
+        raw = rt.raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{name}: stream on {stream.device}, tensors on {tensors[0].device}")
+    else:
         raw = stream.cuda_stream
         if raw != rt.raw_stream(dev):
             for t in tensors:  # their memory is not given away before the work on this stream is done
                 if t is not None:
                     t.record_stream(stream)
-    else:
-        raw = rt.raw_stream(dev)
-    if dev != rt.current_device():
-        with rt.torch.cuda.device(dev):
-            rc = fn(*args, raw)
-    else:
-        rc = fn(*args, raw)
-    if rc != DIT_OK:
-        raise DitError(rc, f"{name}: {status_string(rc)}")
+    with rt.torch.cuda.device(dev):
+        return fn(*args, raw)
+
+
+def _refused(name: str, rc: int):
+    raise DitError(rc, f"{name}: {status_string(rc)}")
 
 
 def _fresh(like, shape, dtype, stream):
     """An output on like's device, from the stream that will write it."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if dtype == like.dtype else like.new_empty(shape, dtype=dtype)
     with _rt().torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
@@ -407,34 +408,49 @@ def linear_fused(x, w, bias=None, act: str = "none", residual=None, out=None, ou
     dtype or float32, residual itself for an update in place; status int32 [1] (zeroed) receives
     a timeout.  Returns out."""
     rt, name = _RT or _rt(), "linear_fused"
-    _need(x.dim() == 2 and w.dim() == 2 and x.shape[1] == w.shape[1], "linear_fused: x [M, K] and w [N, K]")
-    (M, K), N, dtype = x.shape, w.shape[0], x.dtype
-    code = rt.code16.get(dtype)
+    _need(x.dim() == 2 and w.dim() == 2, "linear_fused: x [M, K] and w [N, K]")
+    (M, K), (N, kw), dtype = x.shape, w.shape, x.dtype
+    code, a = rt.code16.get(dtype), ACTIVATIONS.get(act)
     if code is None:
         _no_dtype(name, dtype)
-    _need(w.dtype == dtype, "linear_fused: x and w of one dtype")
-    a = ACTIVATIONS.get(act)
+    if K != kw or w.dtype != dtype:
+        raise ValueError("linear_fused: x [M, K] and w [N, K] of one dtype")
     if a is None:
         raise ValueError(f"linear_fused: act {act!r} is none of {sorted(ACTIVATIONS)}")
-    odtype = (dtype if out is None else out.dtype) if out_dtype is None else out_dtype
-    ocode = rt.code.get(odtype)
+    dev = x.get_device()
+    same = w.get_device() == dev
+    ldx = K if x.is_contiguous() else _row_stride(x, name)
+    ldw = K if w.is_contiguous() else _row_stride(w, name)
+    if out is None:
+        odtype, ldy = dtype if out_dtype is None else out_dtype, N
+    else:
+        odtype, ldy, same = out.dtype, _row_stride(out, name), same and out.get_device() == dev
+        if out.shape != (M, N) or (out_dtype is not None and odtype != out_dtype):
+            raise ValueError("linear_fused: out [M, N] of out_dtype")
+    ocode = code if odtype == dtype else rt.code.get(odtype)
     if ocode is None:
         _no_dtype(name, odtype)
+    pb = pr = ps = None
+    ldr = 0
     if bias is not None:
-        _need(bias.shape == (N,) and bias.dtype == rt.float32 and bias.is_contiguous(), "linear_fused: bias float32 [N]")
-    ldx, ldw, ldr = _row_stride(x, name), _row_stride(w, name), 0
-    if out is None:
-        out, ldy = _fresh(x, (M, N), odtype, stream), N
-    else:
-        _need(out.shape == (M, N) and out.dtype == odtype, "linear_fused: out [M, N] of out_dtype")
-        ldy = _row_stride(out, name)
+        if bias.shape != (N,) or bias.dtype != rt.float32 or not bias.is_contiguous():
+            raise ValueError("linear_fused: bias float32 [N]")
+        pb, same = bias.data_ptr(), same and bias.get_device() == dev
     if residual is not None:
-        _need(residual.shape == (M, N) and residual.dtype == odtype and (residual.stride(1) == 1 or N == 1),
-              "linear_fused: residual [M, N] of out's dtype")
-        ldr = residual.stride(0)
-    _enqueue(rt, name, rt.lib.dit_op_linear_fused, (x, w, out, bias, residual, status), stream,
-             (code, x.data_ptr(), ldx, w.data_ptr(), ldw, None if bias is None else bias.data_ptr(), a,
-              None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy, ocode, M, N, K, _ptr(status)))
+        if residual.shape != (M, N) or residual.dtype != odtype or (residual.stride(1) != 1 and N > 1):
+            raise ValueError("linear_fused: residual [M, N] of out's dtype")
+        pr, ldr, same = residual.data_ptr(), residual.stride(0), same and residual.get_device() == dev
+    if status is not None:
+        ps, same = status.data_ptr(), same and status.get_device() == dev
+    if out is None:
+        out = _fresh(x, (M, N), odtype, stream)
+    args = (code, x.data_ptr(), ldx, w.data_ptr(), ldw, pb, a, pr, ldr, out.data_ptr(), ldy, ocode, M, N, K, ps)
+    if same and stream is None and dev >= 0 and dev == rt.current_device():
+        rc = rt.linear(*args, rt.raw_stream(dev))
+    else:
+        rc = _elsewhere(rt, name, rt.linear, dev, (x, w, out, bias, residual, status), stream, args)
+    if rc != DIT_OK:
+        _refused(name, rc)
     return out
 
 
@@ -458,26 +474,35 @@ def attention_packed(q, k, v, cu_q, cu_k, max_q: int, max_k: int, causal: bool =
     Returns out (rows outside every sequence are not written; a new out starts undefined
     there), or (out, lse float32 [heads, total_q]) with return_lse."""
     rt, name = _RT or _rt(), "attention_packed"
-    _need(q.dim() == 3 and k.dim() == 3 and k.shape == v.shape and q.shape[2] == k.shape[2],
-          "attention_packed: q [total_q, heads, dh], k and v [total_k, kv_heads, dh]")
-    (tq, h, d), (tk, hk, _), dtype = q.shape, k.shape, q.dtype
+    _need(q.dim() == 3 and k.dim() == 3 and k.shape == v.shape, "attention_packed: q [total_q, heads, dh], k and v "
+          "[total_k, kv_heads, dh]")
+    (tq, h, d), (tk, hk, dk), dtype, n = q.shape, k.shape, q.dtype, cu_q.shape[0] - 1
     code = rt.code16.get(dtype)
     if code is None:
         _no_dtype(name, dtype)
-    _need(k.dtype == dtype and v.dtype == dtype, "attention_packed: q, k and v of one dtype")
-    n = cu_q.shape[0] - 1
-    _need(cu_q.dim() == 1 and n >= 0 and cu_k.shape == cu_q.shape and cu_q.dtype == rt.int32 and cu_k.dtype == rt.int32
-          and cu_q.is_contiguous() and cu_k.is_contiguous(), "attention_packed: cu_q and cu_k contiguous int32 [n + 1]")
+    if d != dk or k.dtype != dtype or v.dtype != dtype:
+        raise ValueError("attention_packed: q, k and v of one dtype and feature count")
+    if (cu_q.dim() != 1 or n < 0 or cu_k.shape != cu_q.shape or cu_q.dtype != rt.int32 or cu_k.dtype != rt.int32
+            or not cu_q.is_contiguous() or not cu_k.is_contiguous()):
+        raise ValueError("attention_packed: cu_q and cu_k contiguous int32 [n + 1]")
+    dev = q.get_device()
+    same = (k.get_device() == dev and v.get_device() == dev and cu_q.get_device() == dev and cu_k.get_device() == dev
+            and (out is None or out.get_device() == dev) and (status is None or status.get_device() == dev))
     if out is None:
         out = _fresh(q, (tq, h, d), dtype, stream)
-    else:
-        _need(out.shape == q.shape and out.dtype == dtype, "attention_packed: out like q")
+    elif out.shape != q.shape or out.dtype != dtype:
+        raise ValueError("attention_packed: out like q")
     strides = _Strides8(*_head_strides(q, name), *_head_strides(k, name), *_head_strides(v, name), *_head_strides(out, name))
     lse = _fresh(q, (h, tq), rt.float32, stream) if return_lse else None
-    _enqueue(rt, name, rt.lib.dit_op_attention_packed, (q, k, v, out, lse, cu_q, cu_k, status), stream,
-             (code, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-              cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q, max_k, h, hk, d, strides,
-              d ** -0.5 if scale is None else scale, 1 if causal else 0, _ptr(status)))
+    args = (code, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+            cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q, max_k, h, hk, d, strides,
+            d ** -0.5 if scale is None else scale, 1 if causal else 0, None if status is None else status.data_ptr())
+    if same and stream is None and dev >= 0 and dev == rt.current_device():
+        rc = rt.attention(*args, rt.raw_stream(dev))
+    else:
+        rc = _elsewhere(rt, name, rt.attention, dev, (q, k, v, out, lse, cu_q, cu_k, status), stream, args)
+    if rc != DIT_OK:
+        _refused(name, rc)
     return (out, lse) if return_lse else out
 
 
@@ -520,20 +545,28 @@ class Rotary:
         from that of the result."""
         rt, name = _RT or _rt(), "Rotary.apply"
         _need(x.dim() == 3 and x.shape[2] == self.head_dim, "Rotary.apply: x [tokens, heads, head_dim]")
-        (n, h, d), code = x.shape, rt.code.get(x.dtype)
+        (n, h, d), dtype, wide = x.shape, x.dtype, positions.dtype == rt.int64
+        code = rt.code.get(dtype)
         if code is None:
-            _no_dtype(name, x.dtype)
-        wide = positions.dtype == rt.int64
-        _need((wide or positions.dtype == rt.int32) and positions.is_contiguous()
-              and (positions.shape == (n, self.axes) or (self.axes == 1 and positions.shape == (n,))),
-              "Rotary.apply: positions contiguous int32 or int64 [tokens, axes]")
-        xt, xh = _head_strides(x, name)
+            _no_dtype(name, dtype)
+        if ((not wide and positions.dtype != rt.int32) or not positions.is_contiguous()
+                or (positions.shape != (n, self.axes) and (self.axes != 1 or positions.shape != (n,)))):
+            raise ValueError("Rotary.apply: positions contiguous int32 or int64 [tokens, axes]")
+        dev = x.get_device()
+        same = positions.get_device() == dev and (out is None or out.get_device() == dev)
+        xt, xh = (h * d, d) if x.is_contiguous() else _head_strides(x, name)
         if out is None:
-            out, yt, yh = _fresh(x, (n, h, d), x.dtype, stream), h * d, d
+            out, yt, yh = _fresh(x, (n, h, d), dtype, stream), h * d, d
         else:
-            _need(out.shape == x.shape and out.dtype == x.dtype, "Rotary.apply: out like x")
+            if out.shape != x.shape or out.dtype != dtype:
+                raise ValueError("Rotary.apply: out like x")
             yt, yh = _head_strides(out, name)
-        _enqueue(rt, name, rt.lib.dit_op_rotary, (x, positions, out), stream,
-                 (self._ref, code, x.data_ptr(), xt, xh, positions.data_ptr(), 1 if wide else 0, out.data_ptr(), yt, yh, n, h,
-                  d, self.interleaved, 1 if transpose else 0))
+        args = (self._ref, code, x.data_ptr(), xt, xh, positions.data_ptr(), 1 if wide else 0, out.data_ptr(), yt, yh, n, h, d,
+                self.interleaved, 1 if transpose else 0)
+        if same and stream is None and dev >= 0 and dev == rt.current_device():
+            rc = rt.rotary(*args, rt.raw_stream(dev))
+        else:
+            rc = _elsewhere(rt, name, rt.rotary, dev, (x, positions, out), stream, args)
+        if rc != DIT_OK:
+            _refused(name, rc)
         return out
