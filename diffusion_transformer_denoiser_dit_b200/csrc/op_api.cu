@@ -34,7 +34,14 @@ bool distinct(long long outer, long long so, long long inner, long long si, long
   return (si >= row && so >= si * (inner - 1) + row) || (so >= row && si >= so * (outer - 1) + row);
 }
 
-dit_status launched(cudaError_t e) { return e == cudaSuccess ? DIT_OK : DIT_ERR_CUDA; }
+dit_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return DIT_OK;
+  cudaGetLastError();  // reported here, not to the caller's next CUDA call
+  return DIT_ERR_CUDA;
+}
+
+// sizes leave room for a tile beyond them in 32-bit arithmetic
+constexpr int kMaxSize = 0x7fffffff - 4096;
 
 }  // namespace
 
@@ -47,9 +54,11 @@ dit_status dit_op_linear_fused(int dtype, const void* x, long long ldx, const vo
   if (out_dtype != dtype && out_dtype != DIT_DTYPE_F32) return DIT_ERR_UNSUPPORTED;
   if (M < 0 || N <= 0 || K <= 0 || act < DIT_ACT_NONE || act > DIT_ACT_SILU) return DIT_ERR_INVALID_ARG;
   if (M == 0) return DIT_OK;
+  if (M > kMaxSize || N > kMaxSize || K > kMaxSize) return DIT_ERR_UNSUPPORTED;
   const uintptr_t es = out_dtype == DIT_DTYPE_F32 ? 4 : 2;
   if (x == nullptr || w == nullptr || y == nullptr || ldx < 0 || ldw < 0 || ldr < 0 || (M > 1 && ldy < N) ||
-      !aligned(x, 2) || !aligned(w, 2) || !aligned(bias, 4) || !aligned(y, es) || !aligned(residual, es))
+      !aligned(x, 2) || !aligned(w, 2) || !aligned(bias, 4) || !aligned(y, es) || !aligned(residual, es) ||
+      (y == residual && M > 1 && ldy != ldr))
     return DIT_ERR_INVALID_ARG;
   const int sms = current_sms();
   if (sms == 0) return DIT_ERR_NO_DEVICE;
@@ -82,6 +91,10 @@ dit_status dit_op_attention_packed(int dtype, const void* q, const void* k, cons
       heads % kv_heads != 0 || strides == nullptr || !(scale > 0.f) || !isfinite(scale))
     return DIT_ERR_INVALID_ARG;
   if (dh % 8 != 0 || dh > 128 || heads / kv_heads > 128) return DIT_ERR_UNSUPPORTED;
+  // work items (a query tile of a key head) are counted in 31 bits
+  if (total_k > kMaxSize || max_q > kMaxSize || max_k > kMaxSize ||
+      (static_cast<long long>(total_q) + n_seq) * kv_heads > 0x7fff0000ll)
+    return DIT_ERR_UNSUPPORTED;
   if (n_seq == 0 || total_q == 0) return DIT_OK;
   if (q == nullptr || o == nullptr || cu_q == nullptr || cu_k == nullptr ||
       (total_k > 0 && (k == nullptr || v == nullptr)))
@@ -186,7 +199,7 @@ dit_status dit_op_rotary(const dit_rotary* r, int dtype, const void* x, long lon
       !aligned(x, es) || !aligned(y, es) || !aligned(positions, positions_64bit ? 8 : 4) ||
       !distinct(tokens, y_tok, heads, y_head, dh) || (x == y && (x_tok != y_tok || x_head != y_head)))
     return DIT_ERR_INVALID_ARG;
-  if (static_cast<long long>(heads) * dh > (1 << 24)) return DIT_ERR_UNSUPPORTED;
+  if (static_cast<long long>(heads) * dh > (1 << 24) || tokens > kMaxSize) return DIT_ERR_UNSUPPORTED;
   const int sms = current_sms();
   if (sms == 0) return DIT_ERR_NO_DEVICE;
   RotaryArgs a;

@@ -923,10 +923,8 @@ static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, con
       split = c;
     }
   }
-  // items there can be at most: every sequence ends inside a tile.  Their numbers, a round beyond the last
-  // among them, are 32-bit in the kernel.
+  // items there can be at most: every sequence ends inside a tile
   auto most = [&](long long per) { return (a.total_q / per + a.n_seq) * a.Hk; };
-  if (most(f.TQ) > 0x7fff0000ll) return cudaErrorInvalidValue;
   if (split == 0) {
     e = set_up_fa<NA, T, false>(places);
     if (e != cudaSuccess) return e;

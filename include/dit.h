@@ -409,14 +409,17 @@ enum { DIT_ACT_NONE = 0, DIT_ACT_RELU = 1, DIT_ACT_GELU_TANH = 2, DIT_ACT_GELU =
  *   y[m, n] = act(sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n]
  * x [M, K] rows ldx apart, w [N, K] rows ldw apart: dev, dtype; bias: dev float32 [N] or NULL;
  * act: DIT_ACT_* (GELU_TANH is the tanh form, GELU the erf form); residual [M, N] rows ldr
- * apart, of y's type, or NULL; y [M, N] rows ldy apart: out_dtype = dtype or DIT_DTYPE_F32.
+ * apart (0: one row for all), of y's type, or NULL; y [M, N] rows ldy apart: out_dtype = dtype
+ * or DIT_DTYPE_F32.
  * y may be residual itself (same ldr and ldy: an update in place) and must not overlap
  * anything else.  Sums and epilogue are float32, rounded once at the end; with a float32 y
- * the tensor cores' running sum is moved to registers every 512 products, so that its
- * truncation does not add up over K.  Any M >= 0, N, K >= 1, strides and element alignment;
- * rows of x and w that start on 16-byte boundaries are read by TMA, others by plain loads.
- * DIT_ERR_INVALID_ARG: null pointers, negative sizes or strides, ldy < N, an unknown act.
- * DIT_ERR_UNSUPPORTED: another dtype or out_dtype.
+ * the tensor cores' running sum is taken over in round-to-nearest every 512 products (every
+ * 32nd of K where that is more and the output has few tiles), so that its truncation does
+ * not add up over K.  Any M >= 0, N, K >= 1, strides and element alignment; rows of x and w
+ * that start on 16-byte boundaries are fastest.  Results repeat bit for bit.
+ * DIT_ERR_INVALID_ARG: null pointers, negative sizes or strides, ldy < N, an unknown act, y at
+ * residual's address with another stride.
+ * DIT_ERR_UNSUPPORTED: another dtype or out_dtype, a size above 2^31 - 4097.
  */
 dit_status dit_op_linear_fused(int dtype, const void* x, long long ldx, const void* w, long long ldw, const float* bias,
                                int act, const void* residual, long long ldr, void* y, long long ldy, int out_dtype,
@@ -439,8 +442,9 @@ dit_status dit_op_linear_fused(int dtype, const void* x, long long ldx, const vo
  * nq = 1 is the form for single new tokens over a cache.  The scores stay float32; the
  * probabilities are rounded to dtype for the product with v, their sum is not.  v's rows
  * within a sequence have to be finite (a masked probability is 0, and 0 * inf is NaN).
- * DIT_ERR_UNSUPPORTED: another dtype, dh not a multiple of 8 or above 128, more than 128
- * heads per key head.  DIT_ERR_INVALID_ARG: null pointers, negative sizes, heads not a
+ * Results repeat bit for bit.  DIT_ERR_UNSUPPORTED: another dtype, dh not a multiple of 8 or
+ * above 128, more than 128 heads per key head, (total_q + n_seq) * kv_heads above 2^31 - 65537.
+ * DIT_ERR_INVALID_ARG: null pointers, negative sizes, heads not a
  * multiple of kv_heads, misaligned pointers or strides, o rows that overlap, scale <= 0.
  */
 dit_status dit_op_attention_packed(int dtype, const void* q, const void* k, const void* v, void* o, float* lse,

@@ -545,6 +545,33 @@ def test_layer_of_all_three(lengths, h, hk, d, causal):
     assert (got.double() - want).norm() <= 4 * 2.0 ** -8 * want.norm()
 
 
+def test_first_calls_inside_a_capture():
+    """In a fresh process, so that the kernels' one-time set-up happens while the stream is captured."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from diffusion_transformer_denoiser_dit_b200 import Rotary, attention_packed, linear_fused
+x = torch.randn(600, 4, 64, device="cuda").bfloat16()
+w = torch.randn(512, 256, device="cuda").bfloat16()
+cu, pos = torch.tensor([0, 600], device="cuda").int(), torch.arange(600, device="cuda")
+rot = Rotary(64)
+run = lambda: [linear_fused(attention_packed(rot.apply(x, pos), x, x, cu, cu, m, 600, causal=True).flatten(1)[:n], w)
+               for m, n in ((600, 600), (1, 1), (1, 40))] + [linear_fused(torch.cat([x.flatten(1)] * 9), w)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+for a, b in zip(got, run()):
+    assert torch.equal(a, b) and torch.isfinite(a).all()
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 def test_captured_replayed_and_on_other_streams():
     """The layer captured once and replayed on new inputs, twice at once on two streams, and on a
     side stream, gives the direct call's bits."""

@@ -27,7 +27,8 @@ def linear(**kw):
     (dict(y=None), BAD), (dict(ldx=-1), BAD), (dict(ldw=-8), BAD), (dict(ldr=-8), BAD), (dict(ldy=31), BAD),
     (dict(x=A + 1), BAD), (dict(w=A + 1), BAD), (dict(y=A + 1), BAD), (dict(bias=A + 2), BAD),
     (dict(residual=A + 1), BAD), (dict(out=F32, y=A + 2), BAD), (dict(out=F32, residual=A + 2), BAD),
-    (dict(M=0), OK), (dict(M=0, x=None, y=None), OK),
+    (dict(M=0), OK), (dict(M=0, x=None, y=None), OK), (dict(residual=A, ldr=40), BAD),
+    (dict(M=2 ** 31 - 1), UNS), (dict(N=2 ** 31 - 4096, ldy=2 ** 31), UNS), (dict(K=2 ** 31 - 1), UNS),
 ])
 def test_linear_refusals(change, code):
     assert linear(**change) == code
@@ -55,7 +56,7 @@ def attention(**kw):
     (dict(strides=(256, 64, 128, 64, 128, 0, 256, 64)), BAD),     # key heads that share a row
     (dict(strides=(256, 64, 128, 64, 128, 64, 256, 56)), BAD),    # output heads overlap
     (dict(strides=(256, 64, 128, 64, 128, 64, 192, 64)), BAD),    # output tokens overlap
-    (dict(n=0), OK), (dict(tq=0), OK),
+    (dict(n=0), OK), (dict(tq=0), OK), (dict(tq=2 ** 30 + 2 ** 20), UNS), (dict(tk=2 ** 31 - 1), UNS),
 ])
 def test_attention_refusals(change, code):
     assert attention(**change) == code
@@ -80,7 +81,7 @@ def rotary(r=None, **kw):
     (dict(y=None), BAD), (dict(pos=None), BAD), (dict(x=A + 1), BAD), (dict(dtype=F32, y=A + 2), BAD),
     (dict(pos=A + 2), BAD), (dict(p64=1, pos=A + 4), BAD), (dict(xt=-1), BAD), (dict(yh=-64), BAD),
     (dict(yh=63), BAD), (dict(yt=255), BAD), (dict(xt=512), BAD), (dict(h=1 << 19, y=2 * A, yt=1 << 26), UNS),
-    (dict(n=0), OK),
+    (dict(n=0), OK), (dict(n=2 ** 31 - 1), UNS),
 ])
 def test_rotary_refusals(change, code):
     assert rotary(**change) == code
@@ -130,6 +131,27 @@ def test_rotary_frequencies(pairs, kind, factor):
     assert lib.dit_rotary_init(ctypes.byref(r), f, pairs, 1, amp) == OK
     got = np.array([t / 2.0 ** 64 for t in r.turns[:pairs]]) * 2 * np.pi
     assert np.allclose(got, want, rtol=1e-13, atol=2e-18)
+
+
+def test_quartic_exponential_of_the_attention_kernel():
+    """Its coefficients, read from the source, replayed in float32: 2.7e-6 at most, next to nothing on
+    average, and masked scores (clamped to -126) vanish."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(binding.__file__), "csrc", "op_attention.cu")).read()
+    body = src[src.index("ex2_quartic_f2"):]
+    c = [np.float32(re.search(rf"c{i} = ([0-9.]+)f", body).group(1)) for i in range(5)]
+    x = np.linspace(-125.5, 8.0, 400001, dtype=np.float32)
+    big = np.float32(12582912.0)
+    n = (x + big) - big
+    f = x - n
+    assert np.abs(f).max() <= 0.5
+    p = np.full_like(x, c[4])
+    for k in (3, 2, 1, 0):
+        p = p * f + c[k]
+    got = (p.view(np.int32) + (n.astype(np.int32) << 23)).view(np.float32)
+    rel = got.astype(np.float64) / np.exp2(x.astype(np.float64)) - 1
+    assert np.abs(rel).max() < 2.8e-6 and abs(rel.mean()) < 1e-7
 
 
 def test_fixed_point_angles_are_exact_far_out():
