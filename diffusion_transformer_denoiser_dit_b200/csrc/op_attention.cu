@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(640, 1)
       mbar_init(bar(B::PF + i), 8);               // the group's warps have written P
       mbar_init(bar(B::OD + i), 1);
       mbar_init(bar(B::OF + i), 8);
-      mbar_init(bar(B::XF + i), 4 * f.split);     // partial rows of the cluster's four warps that have rows
+      mbar_init(bar(B::XF + i), 4 * f.split);     // the partial rows of four warps of each CTA
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(bar(B::KF + i), 1);
@@ -722,14 +722,18 @@ __global__ void __launch_bounds__(640, 1)
       } else {
         // Rows go to the CTA that finishes them: CTA r / share keeps rows share * CTA ..; the partial
         // of CTA c, group g is slot 2 c + g: O rows [slot][row][16 n16] float32, then (max, sum) [slot][row].
-        // Few rows: a place of their own that alternates by item, and a barrier that only the warps with rows
-        // meet at; the loads of the next item run on.  (A place is written again two items later, after
-        // the writer passed the next item's barrier, so after every warp finished with this item's rows.)
+        // Few rows: a place of their own that alternates by item, and a barrier that the warps with rows
+        // arrive at; those of group 1, which end last, wait there and finish the rows, while group 0 and
+        // the loads go on with the next item.  A place is written again two items later: before that its
+        // writer has passed the barrier of the item between, where the finishing warps arrived after they
+        // were done with this item's rows.
         // Many rows: the K / V slots, between two barriers of the whole cluster.
         const int rows = min(f.TQ, it.ntok) * f.G, share = (rows + f.split - 1) / f.split;
         const uint32_t wide = (a.dh + 15) / 16 * 64;  // bytes of a row
         const uint32_t part = sbase + (f.light ? C::OFF_X + (n & 1) * C::TILE : C::OFF_KV), stats = part + 2 * f.split * share * wide;
         if (!f.light) cluster_sync_all();
+        else if (g == 0 && q == 0 && n > 0)
+          ok = mbar_wait_cluster(bar(B::XF + ((n - 1) & 1)), ((n - 1) >> 1) & 1, a.status) && ok;
         if (q * 32 < rows) {
           const int owner = min(r / share, f.split - 1), pr = (2 * rank + g) * share + r - owner * share;
           // a row's 16-byte units are rotated by its number: neighbouring rows meet other banks
@@ -759,7 +763,7 @@ __global__ void __launch_bounds__(640, 1)
             __syncwarp();
             if (lane < f.split) mbar_arrive_cluster(mapa_shared(bar(B::XF + (n & 1)), lane));
             __syncwarp();
-            ok = mbar_wait_cluster(bar(B::XF + (n & 1)), (n >> 1) & 1, a.status) && ok;
+            if (g == 1) ok = mbar_wait_cluster(bar(B::XF + (n & 1)), (n >> 1) & 1, a.status) && ok;
             __syncwarp();
           }
         } else {
@@ -767,10 +771,10 @@ __global__ void __launch_bounds__(640, 1)
         }
         // a half-warp per row, eight columns per lane
         const int mrows = min(share, rows - rank * share), u = lane & 15, top = lane & 16;
-        const int step = f.light ? 8 : 32;  // rows per turn: 4 or 16 warps
+        const int step = f.light ? 4 : 32;  // rows per turn: 2 or 16 warps
         const uint32_t slots = 2 * f.split;
 #pragma unroll 1
-        for (int l0 = f.light ? 2 * (2 * g + hf) : 2 * (warp - 4); (!f.light || q == 0) && l0 < mrows; l0 += step) {
+        for (int l0 = f.light ? 2 * hf : 2 * (warp - 4); (!f.light || (q == 0 && g == 1)) && l0 < mrows; l0 += step) {
           const int lr = l0 + (lane >> 4);
           // lane p holds (max, sum) of slot p
           float2 st = make_float2(-INFINITY, 0.f);
@@ -901,7 +905,7 @@ static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, con
                                cudaStream_t st) {
   const PackedAttnArgs& a = f.a;
   // Form and slices, by what was measured in cycles: a key tile step 2600 (either form: two query tiles, or
-  // two key tiles of one), a pair item 5000 besides, a split item 8000; the longest item, or all items over
+  // two key tiles of one), a pair item 5000 besides, a split item 8000 or, with many rows, 13000; the longest item, or all items over
   // the places where they run, whichever lasts longer.  Lengths beyond the longest are averages:
   // the totals are known here, the offsets are not.
   auto tiles = [](long long n, long long per) { return (n + per - 1) / per; };
@@ -914,9 +918,10 @@ static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, con
   const long long pair_all = items(2 * f.TQ) * (nt_avg * 2600 + 5000) / places[0];
   long long best = f.light ? -1 : nt_max * 2600 + 5000 > pair_all ? nt_max * 2600 + 5000 : pair_all;
   int split = 0;  // the pair form
+  const long long extra = f.light ? 8000 : 13000;
   for (int i = 0, c = 1; i < 4; ++i, c *= 2) {
-    long long cost = tiles(nt_max, 2 * c) * 2600 + 8000;
-    const long long all = items(f.TQ) * (tiles(nt_avg, 2 * c) * 2600 + 8000) / places[i];
+    long long cost = tiles(nt_max, 2 * c) * 2600 + extra;
+    const long long all = items(f.TQ) * (tiles(nt_avg, 2 * c) * 2600 + extra) / places[i];
     if (all > cost) cost = all;
     if (best < 0 || cost < best) {
       best = cost;
