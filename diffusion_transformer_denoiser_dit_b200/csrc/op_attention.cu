@@ -234,14 +234,7 @@ __global__ void __launch_bounds__(640, 1)
     if (lane == 0) mbar_arrive(bar(B::IE + (n & 1)));
     return ok && it.ntok >= 0;
   };
-  // A wait that ran out: the role does no more work, but keeps step in the exchanges; what it
-  // issued (copies, products: microseconds) is given a millisecond to end before the block leaves.
-  auto after_timeout = [&]() {
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 1000000u) {
-    }
-    __syncwarp();
-  };
+  // a wait that ran out: the role does no more work, but keeps step in the exchanges
   // split form, many rows: they are exchanged through the K / V slots once every CTA is done with them
   auto exchange_others = [&]() {
     if (SPLIT && !f.light) {
@@ -331,18 +324,18 @@ __global__ void __launch_bounds__(640, 1)
           if (a.n_seq > 1) {
             int rank_of = 0;
 #pragma unroll 4
-          for (int o = 1; o < 32; ++o) {
-            const int other = __shfl_sync(0xffffffffu, lk, (lane + o) & 31);
-            rank_of += other > lk || (other == lk && ((lane + o) & 31) < lane);
-          }
-          volatile int* sorted = reinterpret_cast<volatile int*>(smem + C::OFF_SORT);
-          sorted[rank_of] = lane;
-          __syncwarp();
-          const int from = sorted[lane];
-          __syncwarp();
-          q0 = __shfl_sync(0xffffffffu, q0, from), lq = __shfl_sync(0xffffffffu, lq, from);
-          k0 = __shfl_sync(0xffffffffu, k0, from), lk = __shfl_sync(0xffffffffu, lk, from);
-          tiles = __shfl_sync(0xffffffffu, tiles, from);
+            for (int o = 1; o < 32; ++o) {
+              const int other = __shfl_sync(0xffffffffu, lk, (lane + o) & 31);
+              rank_of += other > lk || (other == lk && ((lane + o) & 31) < lane);
+            }
+            volatile int* sorted = reinterpret_cast<volatile int*>(smem + C::OFF_SORT);
+            sorted[rank_of] = lane;
+            __syncwarp();
+            const int from = sorted[lane];
+            __syncwarp();
+            q0 = __shfl_sync(0xffffffffu, q0, from), lq = __shfl_sync(0xffffffffu, lq, from);
+            k0 = __shfl_sync(0xffffffffu, k0, from), lk = __shfl_sync(0xffffffffu, lk, from);
+            tiles = __shfl_sync(0xffffffffu, tiles, from);
           }
           incl = tiles;
 #pragma unroll
@@ -635,24 +628,24 @@ __global__ void __launch_bounds__(640, 1)
         uint64_t rs2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-        uint32_t pk[16];
+          uint32_t pk[16];
 #pragma unroll
-        for (int i = 16 * h; i < 16 * h + 16; ++i) {
-          const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, nm2);
-          uint64_t p2;
-          if (i % kPolyEvery == kPolyEvery - 1) {
-            p2 = ex2_quartic_f2(x2);
-          } else {
-            float x0, x1;
-            f2_unpack(x2, x0, x1);
-            p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
+          for (int i = 16 * h; i < 16 * h + 16; ++i) {
+            const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, nm2);
+            uint64_t p2;
+            if (i % kPolyEvery == kPolyEvery - 1) {
+              p2 = ex2_quartic_f2(x2);
+            } else {
+              float x0, x1;
+              f2_unpack(x2, x0, x1);
+              p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
+            }
+            rs2[i & 1] = f2_add(rs2[i & 1], p2);
+            float p0, p1;
+            f2_unpack(p2, p0, p1);
+            pk[i - 16 * h] = pack2<T>(p0, p1);
           }
-          rs2[i & 1] = f2_add(rs2[i & 1], p2);
-          float p0, p1;
-          f2_unpack(p2, p0, p1);
-          pk[i - 16 * h] = pack2<T>(p0, p1);
-        }
-        tmem_st16(tS + 16 * h, pk);  // P, in the place of S
+          tmem_st16(tS + 16 * h, pk);  // P, in the place of S
         }
         tmem_st_wait();
         tc_fence_before();

@@ -82,6 +82,15 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, in
   return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, status));
 }
 
+// After a wait that ran out: what the warp issued (copies, products: microseconds) gets a millisecond to end
+// before the block leaves its memory.
+__device__ __forceinline__ void after_timeout() {
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < 1000000u) {
+  }
+  __syncwarp();
+}
+
 // Instruction descriptor, kind::f16: A and B both fp16 or both bf16, K-major, f32 accumulator.
 template <typename T>
 __host__ __device__ constexpr uint32_t idesc_16(int M, int N) {

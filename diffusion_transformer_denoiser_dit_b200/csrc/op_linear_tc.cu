@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(384, 1)
           ph ^= 1u;
         }
       }
+      if (!ok) after_timeout();
     } else if (warp == 1 && leader) {  // ---------------- MMA issuer
       constexpr uint32_t idesc = idesc_16<T>(256, BN);
       int s = 0, it = 0;
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(384, 1)
       // every epilogue release, the partner's remote arrivals among them, has landed
       for (int i = it >= 2 ? it - 2 : 0; i < it && ok; ++i)
         if (!mbar_wait_warp(TEMPTY(i & 1), (i >> 1) & 1, a.status)) break;
+      if (!ok) after_timeout();
     }
   } else {  // ------------------------ epilogue warps 4..11 (both CTAs)
     regs_inc<C::REG_EPI>();
