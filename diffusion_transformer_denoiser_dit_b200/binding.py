@@ -321,8 +321,10 @@ def linear_e4m3(x8, w8, sx, sw, b, block_n: int = 128, stream=None):
 
 
 # ---------------------------------------------------------------- building blocks of packed layers
-# A call's own kernel may last three microseconds, so these look at each argument once and take
-# torch's raw stream and device handles instead of building Stream and device objects.
+# A call's own kernel may last three microseconds, so the common call goes through _fastcall (None from
+# it: nothing was done, the code below decides), and the others look at each argument once and take torch's
+# raw stream and device handles instead of building Stream and device objects.  A linear call of one
+# token then takes the host 4.4 us instead of 9.3, one of attention over 100 keys 8.7 instead of 12.8.
 
 _Strides8 = c_longlong * 8
 _RT = None
@@ -339,6 +341,13 @@ class _Runtime:
         self.code16 = {torch.bfloat16: DIT_DTYPE_BF16, torch.float16: DIT_DTYPE_FP16}
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent without CUDA
         self.current_device = getattr(torch._C, "_cuda_getDevice", None)
+        try:
+            from . import _fastcall as fast
+        except ImportError:  # no headers to build it with, or another torch's
+            fast = None
+        else:
+            fast.bind(*(ctypes.cast(f, c_void_p).value for f in (self.linear, self.attention, self.rotary)))
+        self.fast = fast
 
 
 def _rt() -> _Runtime:
@@ -346,6 +355,13 @@ def _rt() -> _Runtime:
     if _RT is None:
         _RT = _Runtime()
     return _RT
+
+
+def _sizes(name: str, *sizes):
+    """The C interface counts in int; ctypes would drop the upper bits."""
+    worst = max(sizes, key=abs)
+    if abs(worst) > 0x7fffffff:
+        raise ValueError(f"{name}: size {worst} is beyond 32 bits")
 
 
 def _need(ok: bool, what: str):
@@ -408,6 +424,10 @@ def linear_fused(x, w, bias=None, act: str = "none", residual=None, out=None, ou
     dtype or float32, residual itself for an update in place; status int32 [1] (zeroed) receives
     a timeout.  Returns out."""
     rt, name = _RT or _rt(), "linear_fused"
+    if rt.fast is not None and stream is None and status is None:
+        y = rt.fast.linear(x, w, bias, ACTIVATIONS.get(act, -1), residual, out, out_dtype)
+        if y is not None:
+            return y if type(y) is not int else _refused(name, y)
     _need(x.dim() == 2 and w.dim() == 2, "linear_fused: x [M, K] and w [N, K]")
     (M, K), (N, kw), dtype = x.shape, w.shape, x.dtype
     code, a = rt.code16.get(dtype), ACTIVATIONS.get(act)
@@ -417,6 +437,7 @@ def linear_fused(x, w, bias=None, act: str = "none", residual=None, out=None, ou
         raise ValueError("linear_fused: x [M, K] and w [N, K] of one dtype")
     if a is None:
         raise ValueError(f"linear_fused: act {act!r} is none of {sorted(ACTIVATIONS)}")
+    _sizes(name, M, N, K)
     dev = x.get_device()
     same = w.get_device() == dev
     ldx = K if x.is_contiguous() else _row_stride(x, name)
@@ -474,6 +495,10 @@ def attention_packed(q, k, v, cu_q, cu_k, max_q: int, max_k: int, causal: bool =
     Returns out (rows outside every sequence are not written; a new out starts undefined
     there), or (out, lse float32 [heads, total_q]) with return_lse."""
     rt, name = _RT or _rt(), "attention_packed"
+    if rt.fast is not None and stream is None and status is None:
+        y = rt.fast.attention(q, k, v, cu_q, cu_k, max_q, max_k, causal, scale, out, return_lse)
+        if y is not None:
+            return y if type(y) is not int else _refused(name, y)
     _need(q.dim() == 3 and k.dim() == 3 and k.shape == v.shape, "attention_packed: q [total_q, heads, dh], k and v "
           "[total_k, kv_heads, dh]")
     (tq, h, d), (tk, hk, dk), dtype, n = q.shape, k.shape, q.dtype, cu_q.shape[0] - 1
@@ -485,6 +510,7 @@ def attention_packed(q, k, v, cu_q, cu_k, max_q: int, max_k: int, causal: bool =
     if (cu_q.dim() != 1 or n < 0 or cu_k.shape != cu_q.shape or cu_q.dtype != rt.int32 or cu_k.dtype != rt.int32
             or not cu_q.is_contiguous() or not cu_k.is_contiguous()):
         raise ValueError("attention_packed: cu_q and cu_k contiguous int32 [n + 1]")
+    _sizes(name, tq, tk, h, hk, d, n, max_q, max_k)
     dev = q.get_device()
     same = (k.get_device() == dev and v.get_device() == dev and cu_q.get_device() == dev and cu_k.get_device() == dev
             and (out is None or out.get_device() == dev) and (status is None or status.get_device() == dev))
@@ -532,7 +558,7 @@ class Rotary:
                                                    int(original_length), f, ctypes.byref(amp)), "dit_rotary_frequencies")
         self._plan = RotaryPlan()
         self._check(lib.dit_rotary_init(ctypes.byref(self._plan), f, each, self.axes, amp), "dit_rotary_init")
-        self._ref = ctypes.byref(self._plan)
+        self._ref, self._address = ctypes.byref(self._plan), ctypes.addressof(self._plan)
 
     @staticmethod
     def _check(rc: int, what: str):
@@ -544,6 +570,10 @@ class Rotary:
         [tokens, axes] (int32 or int64); out=x turns in place.  transpose: the gradient of x
         from that of the result."""
         rt, name = _RT or _rt(), "Rotary.apply"
+        if rt.fast is not None and stream is None:
+            y = rt.fast.rotary(self._address, self.head_dim, self.axes, self.interleaved, x, positions, out, transpose)
+            if y is not None:
+                return y if type(y) is not int else _refused(name, y)
         _need(x.dim() == 3 and x.shape[2] == self.head_dim, "Rotary.apply: x [tokens, heads, head_dim]")
         (n, h, d), dtype, wide = x.shape, x.dtype, positions.dtype == rt.int64
         code = rt.code.get(dtype)
@@ -552,6 +582,7 @@ class Rotary:
         if ((not wide and positions.dtype != rt.int32) or not positions.is_contiguous()
                 or (positions.shape != (n, self.axes) and (self.axes != 1 or positions.shape != (n,)))):
             raise ValueError("Rotary.apply: positions contiguous int32 or int64 [tokens, axes]")
+        _sizes(name, n, h, d)
         dev = x.get_device()
         same = positions.get_device() == dev and (out is None or out.get_device() == dev)
         xt, xh = (h * d, d) if x.is_contiguous() else _head_strides(x, name)

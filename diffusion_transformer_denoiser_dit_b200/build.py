@@ -2,14 +2,17 @@
 
 Usage: python -m diffusion_transformer_denoiser_dit_b200.build
 Objects go to _build/ at the repository root; the shared library is written next
-to this file so it travels with the package.
+to this file so it travels with the package, and so is _fastcall.so, the short way of binding.py
+into it, where Python's and torch's headers are at hand (binding.py does without it otherwise).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdit_b200.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -59,13 +63,28 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         if verbose or ptxas_verbose or r.returncode != 0:
             sys.stdout.write(r.stdout + r.stderr)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed: " + " ".join(cmd))
+            raise RuntimeError("compiler failed: " + " ".join(cmd))
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         list(ex.map(run, jobs))
     if jobs or _needs(LIB, objs):
         run([nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", LIB] + objs + ["-lcudart_static", "-ldl", "-lrt", "-lpthread"])
+    build_fastcall(run)
     return LIB
+
+
+def build_fastcall(run):
+    spec, python = importlib.util.find_spec("torch"), sysconfig.get_paths()["include"]
+    if spec is None or shutil.which("g++") is None or not os.path.exists(os.path.join(python, "Python.h")):
+        return
+    torch = os.path.dirname(spec.origin)
+    inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    src = os.path.join(CSRC, "fastcall.cpp")
+    if _needs(FASTCALL, [src, os.path.join(INCLUDE, "dit.h"), os.path.join(torch, "version.py")]):
+        cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+        run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE, "-I", python, "-isystem", inc, "-isystem",
+             os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, src, "-o", FASTCALL, "-L", lib,
+             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
 
 
 if __name__ == "__main__":

@@ -9,7 +9,7 @@ import math
 import pytest
 import torch
 
-from diffusion_transformer_denoiser_dit_b200 import DitError, Rotary, attention_packed, linear_fused
+from diffusion_transformer_denoiser_dit_b200 import DitError, Rotary, attention_packed, binding, linear_fused
 
 pytestmark = pytest.mark.gpu
 
@@ -614,3 +614,125 @@ def test_captured_replayed_and_on_other_streams():
         y = layer(cache, w, cu, 200, pos, h, hk, d, rot, True)
     side.synchronize()
     assert torch.equal(y, want[2])
+
+
+# ------------------------------------------------------------------ the two ways from Python
+
+
+def both_ways(call, monkeypatch):
+    """(result by the short way, by the long one, whether the short one took the call)."""
+    rt = binding._rt()
+    taken, fast = [], rt.fast
+
+    class Watch:
+        def __getattr__(self, name):
+            def run(*args):
+                y = getattr(fast, name)(*args)
+                taken.append(y is not None)
+                return y
+            return run
+
+    with monkeypatch.context() as m:
+        m.setattr(rt, "fast", Watch())
+        a = call()
+        m.setattr(rt, "fast", None)
+        b = call()
+    assert len(taken) == 1
+    return a, b, taken[0]
+
+
+def need_short_way():
+    if binding._rt().fast is None:
+        pytest.skip("the short way was not built here")
+
+
+def test_short_way_of_linear(monkeypatch):
+    need_short_way()
+    g = gen(5)
+    x, w, b, r = normal(g, 70, 136, dtype=BF16), normal(g, 96, 136, dtype=BF16), normal(g, 96), normal(g, 70, 96, dtype=BF16)
+    wide = normal(g, 70, 200, dtype=BF16)
+    out = torch.empty(70, 96, device="cuda", dtype=BF16)
+    calls = {
+        "plain": lambda: linear_fused(x, w),
+        "all": lambda: linear_fused(x, w, b, "gelu", r),
+        "row": lambda: linear_fused(x, w, residual=r[:1].expand(70, 96)),
+        "strided": lambda: linear_fused(wide[:, 8:144], w, b, out=torch.zeros_like(wide)[:, 40:136]),
+        "one": lambda: linear_fused(x[3:4], w, b, "silu"),
+        "none": lambda: linear_fused(x[:0], w, b),
+        "f32": lambda: linear_fused(x, w, b, out_dtype=F32),
+        "fp16": lambda: linear_fused(x.to(FP16), w.to(FP16), b, out_dtype=F32, residual=r.to(F32)),
+        "parameter": lambda: linear_fused(x, torch.nn.Parameter(w), torch.nn.Parameter(b)),
+    }
+    for what, call in calls.items():
+        a, want, short = both_ways(call, monkeypatch)
+        assert short and a.dtype == want.dtype and a.stride() == want.stride() and torch.equal(a, want), what
+        assert not a.requires_grad
+    a, _, short = both_ways(lambda: linear_fused(x, w, b, out=out), monkeypatch)
+    assert short and a is out
+    stream = torch.cuda.current_stream()
+    assert torch.equal(linear_fused(x, w, b, stream=stream), linear_fused(x, w, b))
+
+
+def test_short_way_of_attention_and_rotary(monkeypatch):
+    need_short_way()
+    g = gen(6)
+    qkv = normal(g, 90, 8, 64, dtype=BF16)
+    q, k, v = qkv[:, :4], qkv[:, 4:6], qkv[:, 6:]
+    cu = offsets([40, 0, 50])
+    calls = {
+        "plain": lambda: attention_packed(q, k, v, cu, cu, 50, 50),
+        "causal": lambda: attention_packed(q, k, v, cu, cu, 50, 50, True, 0.2),
+        "out": lambda: attention_packed(q, k, v, cu, cu, 50, 50, out=torch.zeros_like(qkv)[:, 2:6]),
+    }
+    for what, call in calls.items():
+        a, want, short = both_ways(call, monkeypatch)
+        assert short and a.stride() == want.stride() and torch.equal(a, want), what
+    (a, la), (want, lw), short = both_ways(lambda: attention_packed(q, k, v, cu, cu, 50, 50, return_lse=True), monkeypatch)
+    assert short and torch.equal(a, want) and torch.equal(la, lw) and la.dtype == F32
+    pos = torch.arange(90, device="cuda")
+    grid = torch.stack([pos // 9, pos % 9], 1).int()
+    for rot, p in ((Rotary(64), pos), (Rotary(64, rotary_dim=32, interleaved=True, axes=2), grid)):
+        for call in (lambda: rot.apply(q, p), lambda: rot.apply(q.float(), p, transpose=True),
+                     lambda: rot.apply(k, p, out=torch.zeros_like(qkv)[:, :2])):
+            a, want, short = both_ways(call, monkeypatch)
+            assert short and a.stride() == want.stride() and torch.equal(a, want)
+
+
+def test_short_way_leaves_refusals_to_the_long_one(monkeypatch):
+    """What the short way does not take raises what the long way raises; a refusal of the library
+    is raised by both."""
+    need_short_way()
+    g = gen(7)
+    x, w = normal(g, 8, 64, dtype=BF16), normal(g, 32, 64, dtype=BF16)
+    q, cu = normal(g, 8, 2, 64, dtype=BF16), offsets([8])
+    rot, pos = Rotary(64), torch.arange(8, device="cuda")
+    bad = [
+        lambda: linear_fused(x, w[:, :32]),
+        lambda: linear_fused(x.float(), w.float()),
+        lambda: linear_fused(x, w.cpu()),
+        lambda: linear_fused(x, w, act="square"),
+        lambda: linear_fused(x, w, bias=torch.zeros(32, device="cuda", dtype=BF16)),
+        lambda: linear_fused(x, w, residual=torch.zeros(8, 32, device="cuda")),
+        lambda: linear_fused(x, w.t().contiguous().t()),
+        lambda: linear_fused(x, w, out=torch.empty(8, 32, device="cuda", dtype=BF16), out_dtype=F32),
+        lambda: linear_fused(x, w, out_dtype=torch.int32),
+        lambda: attention_packed(q, q[:, :, :32], q, cu, cu, 8, 8),
+        lambda: attention_packed(q, q, q, cu.long(), cu.long(), 8, 8),
+        lambda: attention_packed(q, q, q, cu, cu, -1, 8),
+        lambda: attention_packed(q, q, q, cu, cu, 2 ** 40, 8),
+        lambda: attention_packed(q[:, :1], q, q, cu, cu, 8, 8),
+        lambda: rot.apply(q, pos.float()),
+        lambda: rot.apply(q, pos[:4]),
+        lambda: rot.apply(q[:, :, :32], pos),
+    ]
+    rt = binding._rt()
+    for i, call in enumerate(bad):
+        raised = []
+        for fast in (rt.fast, None):
+            with monkeypatch.context() as m:
+                m.setattr(rt, "fast", fast)
+                with pytest.raises(Exception) as e:
+                    call()
+                raised.append((e.type, str(e.value)))
+        assert raised[0] == raised[1], i
+    torch.cuda.synchronize()

@@ -198,3 +198,21 @@ def test_binding_refuses_before_the_library():
             bad()
     with pytest.raises(binding.DitError):
         Rotary(64, scaling="yarn", factor=2.0)       # needs original_length
+
+
+@pytest.mark.parametrize("far", [2 ** 31, 2 ** 32 + 5, 2 ** 40])
+def test_binding_refuses_sizes_beyond_the_interface(far):
+    """Sizes go to the library as int; more must not arrive as their lower bits."""
+    x, w = torch.zeros(1, 64, dtype=torch.bfloat16), torch.zeros(32, 64, dtype=torch.bfloat16)
+    many = x.expand(far, 64)
+    for call in (lambda: linear_fused(many, w), lambda: linear_fused(w, many)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    q, cu = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    for limits in ((far, 4), (4, far), (-far, 4)):
+        with pytest.raises(ValueError, match="32 bits"):
+            attention_packed(q, q, q, cu, cu, *limits)
+    with pytest.raises(ValueError, match="32 bits"):
+        attention_packed(q[:1].expand(far, 2, 64), q, q, cu, cu, 4, 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        Rotary(64).apply(q[:1].expand(far, 2, 64), torch.empty(far, dtype=torch.int32, device="meta"))
