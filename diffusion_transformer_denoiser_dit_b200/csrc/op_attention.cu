@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(640, 1)
         while (sb < a.n_seq && t >= cum + total) {
           cum += total;
           sb += 32;
+          if (sb >= a.n_seq) break;
           const int s = sb + lane;
           q0 = lq = k0 = lk = tiles = 0;
           if (s < a.n_seq) {  // offsets beyond the totals are cut: nothing outside the tensors is used
@@ -322,13 +323,19 @@ __global__ void __launch_bounds__(640, 1)
           }
           // longest first within the 32: lane i takes the sequence of rank i
           if (a.n_seq > 1) {
+            // (lengths read from shared memory, four at once: by 31 shuffles the first item came 1.5 us later)
+            volatile int* sorted = reinterpret_cast<volatile int*>(smem + C::OFF_SORT);
+            sorted[lane] = lk;
+            __syncwarp();
             int rank_of = 0;
 #pragma unroll 4
-            for (int o = 1; o < 32; ++o) {
-              const int other = __shfl_sync(0xffffffffu, lk, (lane + o) & 31);
-              rank_of += other > lk || (other == lk && ((lane + o) & 31) < lane);
+            for (int o = 0; o < 32; o += 4) {
+              const uint4 v = ld_shared_v4(sbase + C::OFF_SORT + 4 * o);
+              const int l4[4] = {static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w)};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) rank_of += l4[e] > lk || (l4[e] == lk && o + e < lane);
             }
-            volatile int* sorted = reinterpret_cast<volatile int*>(smem + C::OFF_SORT);
+            __syncwarp();
             sorted[rank_of] = lane;
             __syncwarp();
             const int from = sorted[lane];
@@ -373,15 +380,15 @@ __global__ void __launch_bounds__(640, 1)
             e.t1 = e.ntok > f.TQ ? seen(e.ntok - 1) : 0;
           }
         }
-        if (!mbar_wait_warp(bar(B::IE + (n & 1)), ((n >> 1) & 1) ^ 1, a.status)) break;
-        if (elect_one()) {
+        const bool room = mbar_wait_warp(bar(B::IE + (n & 1)), ((n >> 1) & 1) ^ 1, a.status);
+        if (room && elect_one()) {
           volatile FaItem& s = items[n & 1];
           s.tok0 = e.tok0, s.ntok = e.ntok, s.k0 = e.k0, s.nk = e.nk, s.off = e.off, s.hk = e.hk, s.t0 = e.t0, s.t1 = e.t1;
           mbar_arrive(bar(B::IF + (n & 1)));
         }
         __syncwarp();
-        if (e.ntok < 0) break;
-        exchange_others();
+        if (n > 0) exchange_others();  // of the item before: this one was looked up meanwhile
+        if (!room || e.ntok < 0) break;
       }
     } else if (warp == 1) {  // ---------------- MMA issue
       // One warp issues for both groups in turn, O_g += P_g V_j and S_g = Q_g K_j+1 of one before those of
@@ -406,7 +413,6 @@ __global__ void __launch_bounds__(640, 1)
         }
       };
       auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && mbar_wait_warp(b, parity, a.status); };
-      FaItem nx;  // read while the current item still runs
       bool more = next_item(0, it);
       for (int n = 0; more; ++n) {
         const int qb = n % C::QB;
@@ -490,7 +496,6 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
           for (int g = 0; g < 2; ++g)
             if (mine[g] > 0) k_of(g);
-          if (f.light) more = next_item(n + 1, nx);
           for (int j = 0; j < all; ++j) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -514,7 +519,6 @@ __global__ void __launch_bounds__(640, 1)
             release(bar(B::KE + kslot[0]));
             step2(kslot[0], kph[0]);
           }
-          more = next_item(n + 1, nx);
           for (int j = 0; j < all; ++j) {
             const int kat = kslot[0], vat = vslot[0];
             if (j + 1 < all) wait(bar(B::KF + kat), kph[0]);
@@ -537,9 +541,8 @@ __global__ void __launch_bounds__(640, 1)
         if (all <= 1) release(bar(B::QE + qb));
 #pragma unroll
         for (int g = 0; g < 2; ++g) ni[g] += mine[g] > 0;
+        more = next_item(n + 1, it);
         exchange_others();
-        if (SPLIT && !f.light) more = next_item(n + 1, nx);
-        it = nx;
       }
       if (!ok) after_timeout();
     } else {  // ---------------- warp 2 only keeps step
