@@ -158,6 +158,9 @@ __device__ __forceinline__ float2 ld_shared_f2(uint32_t addr) {
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void st_shared_f1(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 // wait for arrivals from other CTAs of the cluster and see what they wrote before them
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int* status) {
@@ -765,12 +768,68 @@ __global__ void __launch_bounds__(640, 1)
         } else {
           cluster_sync_all();
         }
-        // a half-warp per row, eight columns per lane
-        const int mrows = min(share, rows - rank * share), u = lane & 15, top = lane & 16;
-        const int step = f.light ? 4 : 32;  // rows per turn: 2 or 16 warps
-        const uint32_t slots = 2 * f.split;
+        const int mrows = min(share, rows - rank * share);
+        const uint32_t slots = 2 * f.split, skip = (share * 16) % wide;
+        if (!f.light) {
+          // Many rows: a thread per row turns its slots' (max, sum) into weights in their place (-1: nothing
+          // seen, its O row was not written) and slot 0's sum into the factor; then eight columns per
+          // thread.  (With both done by a half-warp per row, four rows deep, they took 6600 cycles for a
+          // tile on one CTA.)
+          const int i = threadIdx.x - 128;
+          if (i < mrows) {
+            float mx = -INFINITY, sum = 0.f;
+#pragma unroll 4
+            for (uint32_t p = 0; p < slots; ++p) mx = fmaxf(mx, ld_shared_f2(stats + (p * share + i) * 8).x);
+#pragma unroll 2
+            for (uint32_t p = 0; p < slots; ++p) {
+              const uint32_t at = stats + (p * share + i) * 8;
+              const float2 st = ld_shared_f2(at);
+              const float w = st.x == -INFINITY ? -1.f : ex2_approx(st.x - mx);
+              if (!(w < 0.f)) sum += w * st.y;
+              st_shared_f1(at, w);
+            }
+            const bool any = mx != -INFINITY;
+            st_shared_f1(stats + i * 8 + 4, any ? 1.0f / sum : 0.f);
+            if (a.lse) {
+              const int row = rank * share + i, t = row / f.G, hd = it.hk * f.G + row - t * f.G;
+              a.lse[static_cast<long long>(hd) * a.total_q + it.tok0 + t] = any ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+            }
+          }
+          named_barrier_sync(10, 512);
+          constexpr int LPR = NA == 1 ? 8 : 16;  // threads per row
+          const int u = i % LPR;
+          if (8 * u < a.dh) {
+#pragma unroll 2
+            for (int lr = i / LPR; lr < mrows; lr += 512 / LPR) {
+              float o[8] = {};
+              uint32_t pr = lr, turn = (lr * 16) % wide;
+#pragma unroll 2
+              for (uint32_t p = 0; p < slots; ++p, pr += share) {
+                const float w = ld_shared_f2(stats + pr * 8).x;
+                uint32_t a0 = u * 32 + turn, a1 = a0 + 16;
+                if (a0 >= wide) a0 -= wide;
+                if (a1 >= wide) a1 -= wide;
+                turn += skip;
+                if (turn >= wide) turn -= wide;
+                if (w < 0.f) continue;
+                const uint4 x = ld_shared_v4(part + pr * wide + a0), y = ld_shared_v4(part + pr * wide + a1);
+                o[0] += w * __uint_as_float(x.x), o[1] += w * __uint_as_float(x.y);
+                o[2] += w * __uint_as_float(x.z), o[3] += w * __uint_as_float(x.w);
+                o[4] += w * __uint_as_float(y.x), o[5] += w * __uint_as_float(y.y);
+                o[6] += w * __uint_as_float(y.z), o[7] += w * __uint_as_float(y.w);
+              }
+              const float inv = ld_shared_f2(stats + lr * 8).y;
+              const int row = rank * share + lr, t = row / f.G, hd = it.hk * f.G + row - t * f.G;
+              T* out = static_cast<T*>(a.o) + (it.tok0 + t) * a.o_tok + hd * a.o_head + 8 * u;
+              *reinterpret_cast<uint4*>(out) = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                                                          pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+            }
+          }
+        }
+        // few rows: a half-warp per row, eight columns per lane
+        const int u = lane & 15, top = lane & 16;
 #pragma unroll 1
-        for (int l0 = f.light ? 2 * hf : 2 * (warp - 4); (!f.light || (q == 0 && g == 1)) && l0 < mrows; l0 += step) {
+        for (int l0 = 2 * hf; f.light && q == 0 && g == 1 && l0 < mrows; l0 += 4) {
           const int lr = l0 + (lane >> 4);
           // lane p holds (max, sum) of slot p
           float2 st = make_float2(-INFINITY, 0.f);
@@ -784,7 +843,6 @@ __global__ void __launch_bounds__(640, 1)
           for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
           float o[8] = {};
           uint32_t pr = lr, turn = (lr * 16) % wide;
-          const uint32_t skip = (share * 16) % wide;
 #pragma unroll 2
           for (uint32_t p = 0; p < slots; ++p) {
             const float wp = __shfl_sync(0xffffffffu, w, top + p), mp = __shfl_sync(0xffffffffu, st.x, top + p);
