@@ -771,39 +771,40 @@ __global__ void __launch_bounds__(640, 1)
         const int mrows = min(share, rows - rank * share);
         const uint32_t slots = 2 * f.split, skip = (share * 16) % wide;
         if (!f.light) {
-          // Many rows: a thread per row turns its slots' (max, sum) into weights in their place (-1: nothing
-          // seen, its O row was not written) and slot 0's sum into the factor; then eight columns per
-          // thread.  (With both done by a half-warp per row, four rows deep, they took 6600 cycles for a
-          // tile on one CTA.)
-          const int i = threadIdx.x - 128;
-          if (i < mrows) {
-            float mx = -INFINITY, sum = 0.f;
-#pragma unroll 4
-            for (uint32_t p = 0; p < slots; ++p) mx = fmaxf(mx, ld_shared_f2(stats + (p * share + i) * 8).x);
-#pragma unroll 2
-            for (uint32_t p = 0; p < slots; ++p) {
-              const uint32_t at = stats + (p * share + i) * 8;
-              const float2 st = ld_shared_f2(at);
-              const float w = st.x == -INFINITY ? -1.f : ex2_approx(st.x - mx);
-              if (!(w < 0.f)) sum += w * st.y;
+          // Many rows: a thread per row and slot turns (max, sum) into a weight in its place (-1: nothing seen,
+          // its O row was not written), slot 0's sum into the factor; then eight columns per thread.
+          // (With both done by a half-warp per row, four rows deep, they took 6600 cycles for a tile on
+          // one CTA; with a thread per row, 4200 for the 16 slots of eight.)
+          const int i = threadIdx.x - 128, lr0 = i / static_cast<int>(slots);
+          if (i - lane < mrows * static_cast<int>(slots)) {
+            const uint32_t at = stats + ((i & (slots - 1)) * share + min(lr0, mrows - 1)) * 8;
+            const float2 st = ld_shared_f2(at);
+            float mx = st.x;
+            for (uint32_t x = 1; x < slots; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float w = st.x == -INFINITY ? -1.f : ex2_approx(st.x - mx);
+            float sum = w < 0.f ? 0.f : w * st.y;
+            for (uint32_t x = 1; x < slots; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            if (lr0 < mrows) {
               st_shared_f1(at, w);
-            }
-            const bool any = mx != -INFINITY;
-            st_shared_f1(stats + i * 8 + 4, any ? 1.0f / sum : 0.f);
-            if (a.lse) {
-              const int row = rank * share + i, t = row / f.G, hd = it.hk * f.G + row - t * f.G;
-              a.lse[static_cast<long long>(hd) * a.total_q + it.tok0 + t] = any ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+              if ((i & (slots - 1)) == 0) {
+                const bool any = mx != -INFINITY;
+                st_shared_f1(at + 4, any ? 1.0f / sum : 0.f);
+                if (a.lse) {
+                  const int row = rank * share + lr0, t = row / f.G, hd = it.hk * f.G + row - t * f.G;
+                  a.lse[static_cast<long long>(hd) * a.total_q + it.tok0 + t] = any ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                }
+              }
             }
           }
           named_barrier_sync(10, 512);
           constexpr int LPR = NA == 1 ? 8 : 16;  // threads per row
           const int u = i % LPR;
           if (8 * u < a.dh) {
-#pragma unroll 2
+#pragma unroll 1
             for (int lr = i / LPR; lr < mrows; lr += 512 / LPR) {
               float o[8] = {};
               uint32_t pr = lr, turn = (lr * 16) % wide;
-#pragma unroll 2
+#pragma unroll 4
               for (uint32_t p = 0; p < slots; ++p, pr += share) {
                 const float w = ld_shared_f2(stats + pr * 8).x;
                 uint32_t a0 = u * 32 + turn, a1 = a0 + 16;
@@ -811,12 +812,10 @@ __global__ void __launch_bounds__(640, 1)
                 if (a1 >= wide) a1 -= wide;
                 turn += skip;
                 if (turn >= wide) turn -= wide;
-                if (w < 0.f) continue;
                 const uint4 x = ld_shared_v4(part + pr * wide + a0), y = ld_shared_v4(part + pr * wide + a1);
-                o[0] += w * __uint_as_float(x.x), o[1] += w * __uint_as_float(x.y);
-                o[2] += w * __uint_as_float(x.z), o[3] += w * __uint_as_float(x.w);
-                o[4] += w * __uint_as_float(y.x), o[5] += w * __uint_as_float(y.y);
-                o[6] += w * __uint_as_float(y.z), o[7] += w * __uint_as_float(y.w);
+                const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] += w < 0.f ? 0.f : w * __uint_as_float(v[e]);
               }
               const float inv = ld_shared_f2(stats + lr * 8).y;
               const int row = rank * share + lr, t = row / f.G, hd = it.hk * f.G + row - t * f.G;
