@@ -964,17 +964,21 @@ static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, con
   auto tiles = [](long long n, long long per) { return (n + per - 1) / per; };
   const long long avg_q = a.total_q / a.n_seq, avg_k = a.total_k / a.n_seq;
   auto items = [&](long long per) { return a.n_seq * tiles(avg_q > 0 ? avg_q : 1, per) * a.Hk; };
+  // Up to two rounds are whole ones (52 x 3 items on 148 CTAs: 37.6 us, as pairs in one round 33.3); of more, the
+  // long items of one run beside short ones of the next (8192 tokens causal, 3.5 rounds of pairs: 216 us, in the
+  // form that whole rounds would choose 274).  Single tokens wait for memory, which fewer share in the last round.
+  auto rounds = [&](long long n, long long cost, long long at) { return !f.light && n <= 2 * at ? tiles(n, at) * cost : n * cost / at; };
   const long long nt_max = tiles(a.max_k, 128), nt_avg = tiles(avg_k, 128);
   int places[4];
   cudaError_t e = set_up_fa<NA, T, true>(places);
   if (e != cudaSuccess) return e;
-  const long long pair_all = items(2 * f.TQ) * (nt_avg * 2600 + 5000) / places[0];
+  const long long pair_all = rounds(items(2 * f.TQ), nt_avg * 2600 + 5000, places[0]);
   long long best = f.light ? -1 : nt_max * 2600 + 5000 > pair_all ? nt_max * 2600 + 5000 : pair_all;
   int split = 0;  // the pair form
   const long long extra = f.light ? 8000 : 13000;
   for (int i = 0, c = 1; i < 4; ++i, c *= 2) {
     long long cost = tiles(nt_max, 2 * c) * 2600 + extra;
-    const long long all = items(f.TQ) * (tiles(nt_avg, 2 * c) * 2600 + extra) / places[i];
+    const long long all = rounds(items(f.TQ), tiles(nt_avg, 2 * c) * 2600 + extra, places[i]);
     if (all > cost) cost = all;
     if (best < 0 || cost < best) {
       best = cost;
