@@ -985,6 +985,28 @@ static cudaError_t launch_form(const CUtensorMap& tq, const CUtensorMap& tk, con
       split = c;
     }
   }
+  if (f.G <= 16 && a.max_q <= 16 / f.G) {
+    // Few enough rows for the kernel without tiles (csrc/op_attention_rows.cu): a CTA takes 5200 and a step of
+    // 64 keys 1300 (dh to 64) or 1850, three or two CTAs per SM.  It wins where sequences are short (200 x
+    // 300 keys, 16 heads of 64: 160 -> 70 us; 512 keys, 8 of 128: 9.4 -> 7.2) or memory limits both (256 x 1024
+    // keys, 8 of 128: 195 -> 185), the tiles where few sequences are long (60000 keys: 134 against 72).
+    const long long per_step = NA == 1 ? 1300 : 1850, at = (NA == 1 ? 3 : 2) * places[0], n = static_cast<long long>(a.n_seq) * a.Hk;
+    const long long memory = 4ll * a.total_k * a.Hk * a.dh / 3800;
+    long long least = best > memory ? best : memory;
+    int rows_split = 0;
+    for (int c = 1; c <= 8; c *= 2) {
+      long long cost = tiles(a.max_k, 64 * c) * per_step + 5200;
+      const long long one = tiles(avg_k, 64 * c) * per_step + 5200;
+      const long long all = n * c <= 2 * at ? tiles(n * c, at) * one : n * c * one / at;
+      if (all > cost) cost = all;
+      if (memory > cost) cost = memory;
+      if (cost < least || (rows_split == 0 && cost == least)) {
+        least = cost;
+        rows_split = c;
+      }
+    }
+    if (rows_split > 0) return launch_attention_rows(a, rows_split, st);
+  }
   // items there can be at most: every sequence ends inside a tile
   auto most = [&](long long per) { return (a.total_q / per + a.n_seq) * a.Hk; };
   if (split == 0) {

@@ -42,6 +42,8 @@ struct PackedAttnArgs {
   int* status;
 };
 cudaError_t launch_attention_packed(const PackedAttnArgs& a, cudaStream_t st);
+// sequences of few rows (query tokens x at most 16 heads per key head), 16 at a time, by clusters of `split` CTAs
+cudaError_t launch_attention_rows(const PackedAttnArgs& a, int split, cudaStream_t st);
 
 struct RotaryArgs {
   const void *x, *pos;

@@ -376,6 +376,56 @@ def test_attention_repeats_bit_for_bit(ql, kl):
         assert torch.equal(first, run())
 
 
+# few rows per sequence: by clusters of one, two, four and eight (few items, many keys), more sequences than
+# are ordered at one time, sequences of no queries whose keys are NaN, and hints of one query where there are more
+FEW = [
+    ([1], [1], 1), ([1], [16], 1), ([1, 1, 1], [16, 0, 17], 1), ([1, 0, 1, 1], [63, 64, 65, 513], 1), ([2, 1], [1, 4], 2),
+    ([1] * 5, [1000, 1, 130, 999, 64], 1), ([1, 1], [300, 4000], 1), ([3, 7, 1, 0], [200, 3, 640, 20], 1),
+    ([1, 0, 2, 1, 1] * 14, [3, 70, 33, 128, 260] * 14, 2), ([1] * 40, list(range(0, 400, 10)), 1),
+]
+
+
+@pytest.mark.parametrize("ql,kl,hint", FEW)
+@pytest.mark.parametrize("h,hk,d,dtype", [(1, 1, 8, BF16), (4, 4, 64, FP16), (12, 4, 72, BF16), (16, 1, 128, FP16), (10, 2, 104, BF16),
+                                          (16, 2, 40, BF16)])
+def test_attention_of_few_rows(ql, kl, hint, h, hk, d, dtype):
+    g = gen(12)
+    q, k, v = qkv(g, ql, kl, h, hk, d, dtype)
+    at = 0
+    for nq, nk in zip(ql, kl):
+        if nq == 0:
+            k[at:at + nk], v[at:at + nk] = float("nan"), float("inf")
+        at += nk
+    room = 3                                         # keys and queries behind the last sequence
+    k, v = (torch.cat([x, torch.full_like(x[:1].expand(room, -1, -1), float("nan"))]) for x in (k, v)) if sum(kl) else (k, v)
+    for causal in (False, True):
+        want, tol, lse_want, lse_tol = attention_want(q, k, v, ql, kl, causal, d ** -0.5)
+        out = torch.full((sum(ql) + room, h, d), 7.0, device="cuda", dtype=dtype)
+        qq = torch.cat([q, q.new_full((room, h, d), float("nan"))])
+        got, lse = attention_packed(qq, k, v, offsets(ql), offsets(kl), hint, max(kl), causal=causal, out=out, return_lse=True)
+        n = sum(ql)
+        close(got[:n], want, tol, causal)
+        assert (got[n:] == 7).all()
+        none = lse_want == -math.inf
+        assert torch.equal(lse[:, :n] == -math.inf, none)
+        close(lse[:, :n].masked_fill(none, 0), lse_want.masked_fill(none, 0), lse_tol, "lse")
+        again = attention_packed(qq, k, v, offsets(ql), offsets(kl), hint, max(kl), causal=causal)
+        assert torch.equal(again[:n], got[:n])
+
+
+def test_attention_of_few_rows_with_strides_and_large_scores():
+    """Heads and tokens interleaved in memory; scores whose maximum moves by far more than 2^8."""
+    g = gen(13)
+    ql, kl, d = [1, 2, 1], [70, 400, 1], 72
+    buf = normal(g, sum(kl), 2, 4, 80, dtype=BF16, std=6.0)
+    k, v = buf[:, 0, :, :d], buf[:, 1, :, :d]
+    q = normal(g, 12, sum(ql), 96, dtype=BF16, std=6.0).transpose(0, 1)[:, :, :d]
+    out = torch.zeros(sum(ql), 12, 88, device="cuda", dtype=BF16)[:, :, :d]
+    for causal in (False, True):
+        check_attention(q, k, v, ql, kl, causal, out=out)
+        check_attention(q, k, v, ql, kl, causal, scale=3.0, out=out)
+
+
 # ------------------------------------------------------------------ rotary
 
 
