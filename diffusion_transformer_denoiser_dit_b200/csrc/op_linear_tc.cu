@@ -583,6 +583,7 @@ __global__ void __launch_bounds__(192)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  cluster_started();  // the others are waited for before the first partial row is sent
   const uint32_t tmem_base = uniform(*holder);
   pdl_trigger();
   pdl_wait();
@@ -625,6 +626,7 @@ __global__ void __launch_bounds__(192)
         for (int j = 0; j < C::STAGES; ++j)
           if (armed & (1u << j)) mbar_wait_warp(FULL(j), j < s ? ph : ph ^ 1u, a.status);
     }
+    cluster_all_started();
   } else if (warp == 1) {
     // ---------------- MMA issuer
     constexpr uint32_t idesc = idesc_16<T>(128, BN);
@@ -656,6 +658,7 @@ __global__ void __launch_bounds__(192)
     if (elect_one()) mma_commit(done);
     __syncwarp();
     mbar_wait_warp(done, 0, a.status);
+    cluster_all_started();
   } else {  // ------------------------ warps 2..5: gather, then one row of sums per thread
     const int tid = threadIdx.x - 64, q = warp & 3, r = q * 32 + lane;
     if (GATHER && gathered > 0) {
@@ -689,8 +692,9 @@ __global__ void __launch_bounds__(192)
         }
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncwarp();
     }
+    __syncwarp();
+    cluster_all_started();
     // Row r goes to the CTA that finishes it: CTA r / share keeps rows share * CTA .. of the tile,
     // slice after slice.  A short loop: code that runs once per launch costs its fetch.
     if (m0 + q * 32 < a.M && mbar_wait_warp(done, 0, a.status)) {
