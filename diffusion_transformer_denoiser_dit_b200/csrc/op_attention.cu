@@ -38,16 +38,14 @@ namespace dit {
 // unit gives 16 exponentials a cycle and SM, as long for a 128 x 128 tile as its two products at dh = 128.
 constexpr int kPolyEvery = 5;
 
-// 2^x of a pair, x clamped to >= -126: x = n + f with n the nearest integer (adding and subtracting
+// 2^x of a pair, 0 below -126 (a masked probability has to be 0 itself: 2^-126 of a bfloat16 value near the
+// type's largest is 4): x = n + f with n the nearest integer (adding and subtracting
 // 1.5 * 2^23), 2^f by a quartic fitted on [-1/2, 1/2] by reweighted least squares on the relative error (at
 // most 2.7e-6 in float32, 4e-8 on average: the sum of the probabilities is returned in float32 as well), and n
 // added to the exponent field from the low mantissa bits of x + 1.5 * 2^23.
 __device__ __forceinline__ uint64_t ex2_quartic_f2(uint64_t x2) {
   constexpr float c0 = 0.9999992847442627f, c1 = 0.6931217908859253f, c2 = 0.240247443318367f, c3 = 0.05591785907745361f,
                   c4 = 0.009570100344717503f;
-  float a, b;
-  f2_unpack(x2, a, b);
-  x2 = f2_pack(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
   const uint64_t t2 = f2_add(x2, f2_pack(12582912.0f, 12582912.0f));
   const uint64_t n2 = f2_add(t2, f2_pack(-12582912.0f, -12582912.0f));
   const uint64_t fr = f2_fma(n2, f2_pack(-1.0f, -1.0f), x2);
@@ -55,11 +53,12 @@ __device__ __forceinline__ uint64_t ex2_quartic_f2(uint64_t x2) {
   p = f2_fma(p, fr, f2_pack(c2, c2));
   p = f2_fma(p, fr, f2_pack(c1, c1));
   p = f2_fma(p, fr, f2_pack(c0, c0));
-  float lo, hi, tl, th;
+  float a, b, lo, hi, tl, th;
+  f2_unpack(x2, a, b);
   f2_unpack(p, lo, hi);
   f2_unpack(t2, tl, th);
-  return f2_pack(__uint_as_float(__float_as_uint(lo) + (__float_as_uint(tl) << 23)),
-                 __uint_as_float(__float_as_uint(hi) + (__float_as_uint(th) << 23)));
+  return f2_pack(a >= -126.0f ? __uint_as_float(__float_as_uint(lo) + (__float_as_uint(tl) << 23)) : 0.f,
+                 b >= -126.0f ? __uint_as_float(__float_as_uint(hi) + (__float_as_uint(th) << 23)) : 0.f);
 }
 
 template <int NA, bool SPLIT>
