@@ -38,7 +38,7 @@ namespace dit {
 // unit gives 16 exponentials a cycle and SM, as long for a 128 x 128 tile as its two products at dh = 128.
 constexpr int kPolyEvery = 5;
 
-// 2^x of a pair, 0 below -126 (a masked probability has to be 0 itself: 2^-126 of a bfloat16 value near the
+// 2^x of a pair of numbers (a NaN's row has it in its maximum and sum), 0 below -126 (a masked probability has to be 0 itself: 2^-126 of a bfloat16 value near the
 // type's largest is 4): x = n + f with n the nearest integer (adding and subtracting
 // 1.5 * 2^23), 2^f by a quartic fitted on [-1/2, 1/2] by reweighted least squares on the relative error (at
 // most 2.7e-6 in float32, 4e-8 on average: the sum of the probabilities is returned in float32 as well), and n
@@ -598,16 +598,17 @@ __global__ void __launch_bounds__(640, 1)
         }
         float mp[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mp[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+        for (int e = 0; e < 4; ++e) mp[e] = max_nan(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
 #pragma unroll
         for (int i = 8; i < 64; i += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mp[e] = max3f(mp[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
-        const float mx = fmaxf(max3f(mp[0], mp[1], mp[2]), mp[3]) * f.sc;
+          for (int e = 0; e < 4; ++e) mp[e] = max_nan(mp[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
+        const float mx = max_nan(max_nan(mp[0], mp[1], mp[2]), mp[3]) * f.sc;
         // The reference moves only when a row's maximum grew by more than 2^8 (or is the first): the two
-        // warps of the row agree on that by a barrier that also ors, and only then exchange their maxima
-        if (any_of_pair(pair, mx > m_ref + 8.0f)) {
-          const float m_new = fmaxf(m_ref, join(mx, [](float x, float y) { return fmaxf(x, y); }));
+        // warps of the row agree on that by a barrier that also ors, and only then exchange their maxima.  A NaN
+        // maximum stays, and makes every later sum of its row NaN.
+        if (any_of_pair(pair, !(mx <= m_ref + 8.0f))) {
+          const float m_new = reference_max(m_ref, join(mx, [](float x, float y) { return max_nan(x, y); }));
           const float alpha = m_ref == m_new ? 1.0f : ex2_approx(m_ref - m_new);
           m_ref = m_new;
           l *= alpha;
@@ -669,7 +670,8 @@ __global__ void __launch_bounds__(640, 1)
       const int head = it.hk * f.G + rh;
       if constexpr (!SPLIT) {
         if (warp_ok) {
-          const float inv = lim > 0 ? 1.0f / l : 0.f;
+          const bool any = !(l == 0.f);  // some key has a weight (or NaN)
+          const float inv = any ? 1.0f / l : 0.f;
           // 32 columns at a time (each half every other 32): a lane's row is four 16-byte units; four lanes
           // exchange them so that lane i of the four holds unit i of their four rows, and a store covers
           // 64 bytes of each of eight rows instead of 16 of 32
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(640, 1)
               tmem_ld_wait<32>(o);
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                u[i >> 2][i & 3] = lim > 0 ? pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
+                u[i >> 2][i & 3] = any ? pack2<T>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv) : 0u;
             } else {
 #pragma unroll
               for (int i = 0; i < 16; ++i) u[i >> 2][i & 3] = 0u;
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(640, 1)
           }
           if (row_ok && hf == 0 && a.lse)
             a.lse[static_cast<long long>(head) * a.total_q + it.tok0 + tok] =
-                lim > 0 ? (m_ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                any ? (m_ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
         tc_fence_before();
         __syncwarp();
@@ -779,7 +781,7 @@ __global__ void __launch_bounds__(640, 1)
             const uint32_t at = stats + ((i & (slots - 1)) * share + min(lr0, mrows - 1)) * 8;
             const float2 st = ld_shared_f2(at);
             float mx = st.x;
-            for (uint32_t x = 1; x < slots; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            for (uint32_t x = 1; x < slots; x <<= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, x));
             const float w = st.x == -INFINITY ? -1.f : ex2_approx(st.x - mx);
             float sum = w < 0.f ? 0.f : w * st.y;
             for (uint32_t x = 1; x < slots; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -834,7 +836,7 @@ __global__ void __launch_bounds__(640, 1)
           if (u < slots && lr < mrows) st = ld_shared_f2(stats + (u * share + lr) * 8);
           float mx = st.x;
 #pragma unroll
-          for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+          for (int x = 8; x > 0; x >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, x));
           const float w = st.x == -INFINITY ? 0.f : ex2_approx(st.x - mx);
           float sum = w * st.y;
 #pragma unroll

@@ -184,21 +184,21 @@ __global__ void __launch_bounds__(32 * kRowWarps, NA == 1 ? 3 : 2) attention_row
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (key0 + 8 * x + 2 * t + (c & 1) >= lim[c >> 1]) sc[x][c] = -INFINITY;
-          mx[c >> 1] = fmaxf(mx[c >> 1], sc[x][c]);
+          mx[c >> 1] = max_nan(mx[c >> 1], sc[x][c]);
         }
       bool grew = false;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * f.sc;
-        grew = grew || mx[h] > m[h] + 8.0f;
+        mx[h] = max_nan(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = max_nan(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * f.sc;
+        grew = grew || !(mx[h] <= m[h] + 8.0f);
       }
-      // the reference moves only when a maximum grew by more than 2^8 (or is the first)
+      // the reference moves only when a maximum grew by more than 2^8 (or is the first); a NaN maximum stays
       if (__any_sync(0xffffffffu, grew)) {
         float alpha[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float mn = fmaxf(m[h], mx[h]);
+          const float mn = reference_max(m[h], mx[h]);
           alpha[h] = mn == m[h] ? 1.0f : ex2_approx(m[h] - mn);
           m[h] = mn;
           l[h] *= alpha[h];
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, NA == 1 ? 3 : 2) attention_row
       float mx = -INFINITY, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, stat[w][r].x);
+      for (int w = 0; w < kRowWarps; ++w) mx = max_nan(mx, stat[w][r].x);
 #pragma unroll
       for (int w = 0; w < kRowWarps; ++w) {
         const float2 st = stat[w][r];
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, NA == 1 ? 3 : 2) attention_row
       const int r = i / units, c = (i - r * units) * 8;
       const uint32_t at = smem_u32(&joined[r][c]), st_at = smem_u32(&joined_stat[r]);
       float mx = -INFINITY, sum = 0.f, acc[8] = {};
-      for (int p = 0; p < f.split; ++p) mx = fmaxf(mx, ld_cluster_f2(mapa_shared(st_at, p)).x);
+      for (int p = 0; p < f.split; ++p) mx = max_nan(mx, ld_cluster_f2(mapa_shared(st_at, p)).x);
 #pragma unroll 2
       for (int p = 0; p < f.split; ++p) {
         const float2 st = ld_cluster_f2(mapa_shared(st_at, p));

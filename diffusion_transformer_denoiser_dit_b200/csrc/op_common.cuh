@@ -1,6 +1,8 @@
 // Element types of the packed-layer building blocks: loads to and stores from float32.
 #pragma once
 
+#include <math.h>
+
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -89,6 +91,24 @@ __device__ __forceinline__ void after_timeout() {
   while (global_timer_ns() - t0 < 1000000u) {
   }
   __syncwarp();
+}
+
+// Maxima that keep a NaN (fmaxf drops it): a softmax whose maximum forgets a NaN score would lose the row's.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// The new reference maximum of a softmax row: one of +inf (an infinite score, or one that overflowed) becomes
+// NaN, as inf - inf in its exponentials is.
+__device__ __forceinline__ float reference_max(float a, float b) {
+  const float m = max_nan(a, b);
+  return m == INFINITY ? NAN : m;
 }
 
 // Instruction descriptor, kind::f16: A and B both fp16 or both bf16, K-major, f32 accumulator.

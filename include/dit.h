@@ -431,7 +431,8 @@ dit_status dit_op_linear_fused(int dtype, const void* x, long long ldx, const vo
  * cu_k[s] .. cu_k[s+1]-1; for its query i (of nq) and head h,
  *   o_i = sum_j p_ij v_j,  p_ij = softmax_j(scale q_i . k_j),  j over the nk keys of s, or
  *   with causal over j <= i + nk - nq (the last query sees every key),
- * k and v of head h / (heads / kv_heads).  A query that sees no key gets o = 0, lse = -inf.
+ * k and v of head h / (heads / kv_heads).  A query that sees no key, or only scores of -inf, gets
+ * o = 0, lse = -inf; one that sees a NaN or +inf score (one beyond float32 too) gets NaN in both.
  * q, o [total_q, heads, dh]; k, v [total_k, kv_heads, dh]: dev, dtype, features contiguous,
  * 16-byte aligned; strides: host long long[8] = token and head strides of q, k, v, o in
  * elements, multiples of 8.  lse: dev float32 [heads, total_q] (log of the sum of

@@ -3,6 +3,8 @@ finite, the largest ones, long sums, tails (GPU).  What is expected is the defin
 
 Tolerances are counted: u = torch.finfo(t).eps / 2 is the largest relative error of one rounding to t.
 """
+import math
+
 import pytest
 import torch
 
@@ -11,6 +13,11 @@ from diffusion_transformer_denoiser_dit_b200 import attention_packed
 pytestmark = pytest.mark.gpu
 
 BF16, FP16, F32 = torch.bfloat16, torch.float16, torch.float32
+NAN, INF = math.nan, math.inf
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
 
 
 def gen(seed):
@@ -26,6 +33,69 @@ def offsets(lengths):
 
 
 # ------------------------------------------------------------------ attention
+
+
+def attention_want(q, k, v, ql, kl, causal, scale):
+    """out, its tolerance, lse, its tolerance in 64 bits; a row that sees a NaN or +inf score is NaN, one whose
+    scores are all -inf (or that sees no key) is 0 with lse -inf.
+
+    A score is off by ds <= scale sum|q||k| 2^-22 (dh / 16 + 2) (the products' sum in the tensor cores) and by 2^-22
+    of itself and of the row's maximum (scale log2 e in float32, the product, the subtraction of the maximum).  The
+    base-2 exponential is off by 3e-6 of its value (the quartic 2.8e-6, the exponential unit 2^-22), the float32 sum by
+    2^-24 for each of at most nk / 128 + 48 additions.  In the output each of these counts in numerator and
+    sum; a probability is rounded to the type for the product with v: by u of its value, or for fp16 below 2^-14 by 2^-25
+    of a reference that is at most the row's sum; that product's sum drops 2^-22 per 16 keys; then one rounding."""
+    h, hk = q.shape[1], k.shape[1]
+    u = half_step(q.dtype)
+    small = 2.0 ** -25 if q.dtype == FP16 else 0.0
+    outs, tols, logs, ltols = [], [], [], []
+    a = b = 0
+    for nq, nk in zip(ql, kl):
+        qq = q[a:a + nq].double().transpose(0, 1)
+        kk = k[b:b + nk].double().repeat_interleave(h // hk, 1).transpose(0, 1)
+        vv = v[b:b + nk].double().repeat_interleave(h // hk, 1).transpose(0, 1)
+        a, b = a + nq, b + nk
+        s = qq @ kk.transpose(1, 2) * scale
+        if causal:
+            i, j = torch.arange(nq, device="cuda")[:, None], torch.arange(nk, device="cuda")
+            s = s.masked_fill(j > i + nk - nq, -INF)
+        top = s.amax(-1, keepdim=True) if nk else torch.full((h, nq, 1), -INF, dtype=torch.float64, device="cuda")
+        bad = torch.isnan(top) | (top == INF)
+        none = top == -INF
+        z = torch.logsumexp(s.masked_fill(bad, 0), -1, keepdim=True) if nk else top
+        p = torch.exp(s - z.masked_fill(none, 0)).masked_fill(bad, 0)
+        fin = lambda t: torch.nan_to_num(t.abs(), 0, 0, 0)  # noqa: E731
+        ds = fin(qq) @ fin(kk).transpose(1, 2) * scale * 2.0 ** -22 * (q.shape[2] / 16 + 2) + (fin(s) + fin(top)) * 2.0 ** -22
+        add = (nk / 128 + 48) * 2.0 ** -24
+        # a weight of exactly 0 takes nothing of its value, however large that is
+        o = torch.where(p[..., None] > 0, p[..., None] * vv[:, None], 0).sum(-2) if nk < 600 else p @ vv
+        each = p * (2 * (ds + 3e-6 + add) + u + 2.0 ** -22 * (nk / 16 + 4)) + small * (p > 0)
+        err = torch.where(each[..., None] > 0, each[..., None] * vv.abs()[:, None], 0).sum(-2) if nk < 600 else each @ vv.abs()
+        nan = torch.full_like(o, NAN)
+        outs.append(torch.where(bad, nan, torch.where(none, 0 * nan.nan_to_num(0), o)).transpose(0, 1))
+        tols.append((err + (o.abs() + err) * u + torch.finfo(q.dtype).tiny).transpose(0, 1))
+        logs.append(torch.where(bad, torch.full_like(z, NAN), z)[..., 0])
+        ltols.append((p * (ds + 3e-6)).sum(-1) + add + fin(z[..., 0]) * 2.0 ** -21 + 1e-6)
+    return torch.cat(outs), torch.cat(tols), torch.cat(logs, 1), torch.cat(ltols, 1)
+
+
+def same(got, want, tol, what):
+    got = got.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), (what, "NaN", int(torch.isnan(got).sum()), int(torch.isnan(want).sum()))
+    fine = torch.isfinite(want)
+    rest = ~fine & ~torch.isnan(want)
+    assert torch.equal(got[rest], want[rest]), (what, "inf")
+    off = (got[fine] - want[fine]).abs() - tol[fine]
+    assert off.numel() == 0 or off.max() <= 0, (what, off.max().item(), int((off > 0).sum()))
+
+
+def check_attention(q, k, v, ql, kl, causal, scale=None):
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    want, tol, lse_want, lse_tol = attention_want(q, k, v, ql, kl, causal, scale)
+    got, lse = attention_packed(q, k, v, offsets(ql), offsets(kl), max(ql), max(kl), causal=causal, scale=scale, return_lse=True)
+    same(got, want, tol, "out")
+    same(lse, lse_want, lse_tol, "lse")
+    return got, lse
 
 
 # lengths and heads that reach each way through the keys: single tokens (short, and over several CTAs), few rows
@@ -59,3 +129,60 @@ def test_attention_masked_values_have_no_weight(form, d, dtype):
         blind[a - nq:a - nq // 2] = True
     got, lse = run(large)
     assert torch.equal(got[blind], want[blind]) and torch.equal(lse, lse_want)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d,dtype", [(64, BF16), (128, FP16), (72, BF16)])
+@pytest.mark.parametrize("form", sorted(FORMS))
+def test_attention_nan_in_a_query_or_a_key_is_seen(form, d, dtype, causal):
+    q, k, v, ql, kl = inputs(form, d, dtype, d)
+    check_attention(q, k, v, ql, kl, causal)
+    bad = q.clone()
+    bad[0, 0, 1], bad[-1, -1, d - 1] = NAN, NAN
+    got, lse = check_attention(bad, k, v, ql, kl, causal)
+    assert torch.isnan(got[0, 0]).all() and torch.isnan(lse[0, 0]) and torch.isnan(got[-1, -1]).all()
+    # one key at a time, at places of every kind inside a tile; then all of a sequence's
+    for at in (0, 8, 9, 16, kl[0] - 1):
+        bad = k.clone()
+        bad[at, 0, 3] = NAN
+        check_attention(q, bad, v, ql, kl, causal)
+    bad = k.clone()
+    bad[:kl[0], :, 0] = NAN
+    check_attention(q, bad, v, ql, kl, causal)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d,dtype", [(64, FP16), (128, BF16)])
+@pytest.mark.parametrize("form", sorted(FORMS))
+def test_attention_infinite_scores(form, d, dtype, causal):
+    """A key with an infinite feature scores +inf or -inf by the sign of the query's: the first makes the row NaN, the
+    second leaves the key out; a row whose scores are all -inf has no weight on any key."""
+    q, k, v, ql, kl = inputs(form, d, dtype, d + 1)
+    for at in (0, 8, 16, kl[0] - 1):
+        bad = k.clone()
+        bad[at, :, 5] = INF
+        check_attention(q, bad, v, ql, kl, causal)
+    bad = k.clone()
+    bad[:kl[0], :, 5] = INF
+    got, lse = check_attention(q, bad, v, ql, kl, causal)
+    left_out = (q[0, :, 5] < 0)
+    assert left_out.any() and (got[0][left_out] == 0).all() and (lse[left_out, 0] == -INF).all()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("form", sorted(FORMS))
+def test_attention_scores_that_overflow(form, sign):
+    """A score that is finite until it is scaled (64 equal products, 1e38 in all, times 8): as an infinite one.  Of
+    mixed signs, partial sums of such products may overflow on the way, so that nothing is said of those."""
+    q, k, v, ql, kl = inputs(form, 64, BF16, 7)
+    q, k = q.clone(), k.clone()
+    q[0], k[3] = 1.25e18, sign * 1.25e18
+    k[:3], k[4:kl[0]] = k[:3].abs() * 1e-18, k[4:kl[0]].abs() * 1e-18
+    got, lse = attention_packed(q, k, v, offsets(ql), offsets(kl), max(ql), max(kl), scale=8.0, return_lse=True)
+    if sign > 0:
+        assert torch.isnan(got[0]).all() and torch.isnan(lse[:, 0]).all()
+        return
+    keep = [j for j in range(kl[0]) if j != 3]       # that key has no weight, the others theirs
+    want, tol, lse_want, lse_tol = attention_want(q[:1], k[:kl[0]][keep], v[:kl[0]][keep], [1], [kl[0] - 1], False, 8.0)
+    same(got[:1], want, tol, "out")
+    same(lse[:, :1], lse_want, lse_tol, "lse")
