@@ -17,8 +17,8 @@
 //
 // float32 outputs: tcgen05 drops bits below the accumulator's last place at every 16-wide step,
 // a one-sided error that grows with K (5e-6 of the result's norm at K = 4608, where float32
-// summation has 7e-7).  So the sum is taken over in registers every 512 products, in
-// round-to-nearest.  16-bit outputs (rounded at 2^-9 or 2^-12) run all of K in one go.
+// summation has 7e-7).  So the sum is taken over every 512 products, in round-to-nearest: in registers
+// (pairs), or by another accumulator in tensor memory (split K).  16-bit outputs (rounded at 2^-9 or 2^-12) run all of K in one go.
 //
 // Every wait is bounded; no TMA multicast.
 #include <type_traits>
@@ -453,7 +453,8 @@ struct SplitCfg {
   // release) took 1.6 us measured, so 96 KB of stages fed an SM 31 bytes a cycle and no more.
   static constexpr int STAGES = (232448 - 1024 - 256 - PART) / STAGE;
   static constexpr int SMEM = 1024 + STAGES * STAGE + PART + 256;
-  static constexpr int TMEM = 4 * BN;                // up to four accumulators: chunks of a float32 sum
+  static constexpr int TMEM = 4 * BN;                // four accumulators: the first chunk's, which takes over the
+                                                     // later ones of a long sum, and three in turn
   // 16-byte unit u of partial row r: rows 8 apart in one bank group, neighbours in others
   static __device__ __forceinline__ uint32_t part_at(int r, int u) {
     return static_cast<uint32_t>(r) * (BN * 4) + static_cast<uint32_t>((u & ~7) | ((u ^ r) & 7)) * 16;
@@ -551,7 +552,11 @@ __global__ void __launch_bounds__(192)
   auto FULL = [&](int s) { return bar0 + 8u * s; };
   auto EMPTY = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
   const uint32_t done = bar0 + 8u * (2 * C::STAGES);  // the last product of this CTA is complete
-  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::STAGES * C::STAGE + C::PART + 8 * (2 * C::STAGES + 1));
+  // sums of more than four chunks: a chunk is complete; it has been added to the first, its place is free
+  auto CHUNK = [&](int b) { return done + 8u * b; };        // b = 1, 2, 3
+  auto TAKEN = [&](int b) { return done + 8u * (3 + b); };
+  static_assert(8 * (2 * C::STAGES + 7) + 4 <= 256, "barrier area");
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::STAGES * C::STAGE + C::PART + 8 * (2 * C::STAGES + 7));
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int m_tiles = (a.M + 127) / 128;
@@ -560,9 +565,9 @@ __global__ void __launch_bounds__(192)
   const int kblocks_all = (a.K + 63) / 64;
   const int kb_begin = static_cast<int>(static_cast<long long>(kblocks_all) * rank / sp.split);
   const int kb_end = static_cast<int>(static_cast<long long>(kblocks_all) * (rank + 1) / sp.split);
-  // blocks per accumulator: all of them, or 512 products (a quarter of the slice if that is more)
+  // blocks per accumulator: all of them, or 512 products.  Chunk 0 is in accumulator 0, chunk i in 1 + (i - 1) % 3.
   const int nkb = kb_end - kb_begin;
-  const int chunk = a.out_f32 ? max(kF32ChunkBlocks, (nkb + 3) / 4) : nkb;
+  const int chunk = a.out_f32 ? kF32ChunkBlocks : nkb, nchunks = (nkb + chunk - 1) / chunk;
   // rows of the tile that one CTA of the cluster finishes
   const int share = (min(128, a.M - m0) + sp.split - 1) / sp.split;
   const int gathered = GATHER ? (sp.grain_x != 0) + (sp.grain_w != 0) : 0;
@@ -574,6 +579,10 @@ __global__ void __launch_bounds__(192)
       mbar_init(EMPTY(s), 1);
     }
     mbar_init(done, 1);
+    for (int b = 1; b < 4; ++b) {
+      mbar_init(CHUNK(b), 1);
+      mbar_init(TAKEN(b), 4);  // one arrival per warp with rows
+    }
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -630,9 +639,10 @@ __global__ void __launch_bounds__(192)
   } else if (warp == 1) {
     // ---------------- MMA issuer
     constexpr uint32_t idesc = idesc_16<T>(128, BN);
-    int s = 0, left = chunk;
+    int s = 0, left = chunk, i = 0, b = 0;  // chunk i in accumulator b
     uint32_t ph = 0, acc = tmem_base, fresh = 0;
     for (int kb = 0; kb < nkb; ++kb) {
+      if (i >= 4 && fresh == 0 && !mbar_wait_warp(TAKEN(b), ((i - 1) / 3 - 1) & 1, a.status)) break;
       if (!mbar_wait_warp(FULL(s), ph, a.status)) break;
       tc_fence_after();
       const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES;
@@ -645,8 +655,14 @@ __global__ void __launch_bounds__(192)
       __syncwarp();
       fresh = 1;
       if (--left == 0) {
+        if (i > 0 && i + 4 <= nchunks) {
+          if (elect_one()) mma_commit(CHUNK(b));
+          __syncwarp();
+        }
         left = chunk;
-        acc += BN;
+        b = b == 3 ? 1 : b + 1;
+        ++i;
+        acc = tmem_base + b * BN;
         fresh = 0;
       }
       if (++s == C::STAGES) {
@@ -661,14 +677,45 @@ __global__ void __launch_bounds__(192)
     cluster_all_started();
   } else {  // ------------------------ warps 2..5: gather, then one row of sums per thread
     const int tid = threadIdx.x - 64, q = warp & 3, r = q * 32 + lane;
+    // chunk i (0 < i <= nchunks - 4) onto the first accumulator, in the order of the chunks
+    auto take_over = [&](int i) -> bool {
+      const int b = 1 + (i - 1) % 3;
+      if (!mbar_wait_warp(CHUNK(b), ((i - 1) / 3) & 1, a.status)) return false;
+      tc_fence_after();
+      const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 16) {
+        uint32_t v[16], w[16];
+        tmem_ld16(t + c, v);
+        tmem_ld16(t + b * BN + c, w);
+        tmem_ld_wait<16>(v);
+        tmem_ld_wait<16>(w);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(w[e]));
+        tmem_st16(t + c, v);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(TAKEN(b));
+      return true;
+    };
+    if (!(GATHER && gathered > 0))
+      for (int i = 1; i + 4 <= nchunks; ++i)
+        if (!take_over(i)) break;
     if (GATHER && gathered > 0) {
       // copies of up to AHEAD stages are in flight; a stage is handed over when this thread's share landed
       constexpr int AHEAD = 3;
       static_assert(C::STAGES > AHEAD, "stages");
-      int s = 0, full = 0;
+      int s = 0, full = 0, next = 1;  // the next chunk to take over
       uint32_t ph = 0;
       bool ok = true;
       for (int kb = kb_begin; kb < kb_end + AHEAD; ++kb) {
+        // a whole chunk later: all of its stages have been handed over, and its products do not wait for this warp
+        if (next + 4 <= nchunks && kb - kb_begin == (next + 2) * chunk) {
+          ok = __all_sync(0xffffffffu, ok) && take_over(next);
+          ++next;
+        }
         if (kb < kb_end) {
           ok = ok && mbar_wait_spin(EMPTY(s), ph ^ 1u, a.status);
           if (ok) {
@@ -708,9 +755,9 @@ __global__ void __launch_bounds__(192)
         tmem_ld16(t + c, v);
         tmem_ld_wait<16>(v);
 #pragma unroll 1
-        for (int j = chunk; j < nkb; j += chunk) {
+        for (int j = max(1, nchunks - 3); j < nchunks; ++j) {
           uint32_t w[16];
-          tmem_ld16(t + (j / chunk) * BN + c, w);
+          tmem_ld16(t + (1 + (j - 1) % 3) * BN + c, w);
           tmem_ld_wait<16>(w);
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));

@@ -8,7 +8,7 @@ import math
 import pytest
 import torch
 
-from diffusion_transformer_denoiser_dit_b200 import attention_packed
+from diffusion_transformer_denoiser_dit_b200 import attention_packed, linear_fused
 
 pytestmark = pytest.mark.gpu
 
@@ -30,6 +30,59 @@ def normal(g, *shape, dtype=F32, std=1.0):
 
 def offsets(lengths):
     return torch.tensor([0] + lengths, device="cuda").cumsum(0).to(torch.int32)
+
+
+# ------------------------------------------------------------------ linear
+
+
+def same_signed(m, n, k, dtype, std, dx, dw):
+    """Operands of one sign, in rows dx and dw elements longer than K."""
+    g = gen(m + n + k)
+    x = normal(g, m, k + dx, dtype=F32, std=std).abs().to(dtype)[:, :k]
+    w = normal(g, n, k + dw, dtype=F32, std=std).abs().to(dtype)[:, :k]
+    return x, w
+
+
+def long_sum(x, w):
+    """In 64 bits, in parts of K."""
+    return sum(a.double() @ b.double().t() for a, b in zip(x.split(8192, 1), w.split(8192, 1)))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("m,n,k,dx,dw", [
+    (6, 256, 65536, 0, 0), (130, 700, 65536, 0, 0), (1024, 1152, 16384, 0, 0), (1024, 1152, 65536, 0, 0),
+    (1024, 1152, 65535, 0, 0), (1024, 1152, 65536, 4, 2), (2100, 1100, 16390, 1, 0), (4096, 4096, 8190, 0, 0), (9, 72, 40000, 3, 0),
+    (300, 2000, 4672, 0, 0), (1024, 1152, 17000, 0, 8), (2048, 4608, 32768, 0, 0),
+])
+def test_linear_long_float32_sums(m, n, k, dx, dw, dtype):
+    """Products of one sign.  The tensor cores cut off what lies below the sum's last place, of the sum and of each of
+    the 16 products of a step (fp16's reach lower than bf16's), which is one-sided: a sum taken over every 512 products has
+    the mean error of one of 512 products, however long K is.  The roundings to nearest beside it (2^-24 each, at most
+    k / 512 + 8 of them) are of either sign and leave less than one 2^-24 in the mean of a thousand outputs; the
+    last place varies with the value inside a factor of two, which a mean over parts evens out: 1.1.  A single value is off
+    by at most 2^-22 of the sum at each of 32 steps, (33 / 2) 2^-22 of a sum that grows evenly, and all the roundings."""
+    x, w = same_signed(m, n, k, dtype, 0.25, dx, dw)
+
+    def off(x, w):
+        want = long_sum(x, w)
+        return (linear_fused(x, w, out_dtype=F32).double() - want) / want
+
+    # many rows of K = 512: each output's products are in one accumulator (of few, K is cut between CTAs as well)
+    whole, one = off(x, w), off(*same_signed(4096, 4096, 512, dtype, 0.25, 0, 0)).mean().abs()
+    assert whole.mean().abs() <= 1.1 * one + 2.0 ** -24, (whole.mean().item(), one.item())
+    assert whole.abs().max() <= 33 * 2.0 ** -23 + (k / 512 + 8) * 2.0 ** -24, whole.abs().max().item()
+
+
+@pytest.mark.parametrize("m,n,k,dx", [(6, 256, 65536, 0), (1024, 1152, 20000, 0), (1024, 1152, 20001, 1)])
+def test_linear_long_float32_sums_repeat_and_add_the_rest(m, n, k, dx):
+    x, w = same_signed(m, n, k, BF16, 0.25, dx, 0)
+    b, r = normal(gen(1), n, std=100.0), normal(gen(2), m, n, std=100.0)
+    first = linear_fused(x, w, b, act="silu", residual=r, out_dtype=F32)
+    want = long_sum(x, w) + b.double()
+    want = want * torch.sigmoid(want) + r.double()
+    assert ((first.double() - want).abs() / want.abs()).max() <= 40 * 2.0 ** -23 + (k / 512 + 12) * 2.0 ** -24
+    for _ in range(3):
+        assert torch.equal(first, linear_fused(x, w, b, act="silu", residual=r, out_dtype=F32))
 
 
 # ------------------------------------------------------------------ attention
