@@ -413,8 +413,9 @@ enum { DIT_ACT_NONE = 0, DIT_ACT_RELU = 1, DIT_ACT_GELU_TANH = 2, DIT_ACT_GELU =
  * or DIT_DTYPE_F32.
  * y may be residual itself (same ldr and ldy: an update in place) and must not overlap
  * anything else.  Sums and epilogue are float32, rounded once at the end; with a float32 y
- * the tensor cores' running sum is taken over in round-to-nearest every 512 products, so that
- * its truncation does not add up over K.  Any M >= 0, N, K >= 1, strides and element alignment; rows of x and w
+ * the tensor cores' running sum is taken over in round-to-nearest every 512 products, with a
+ * 16-bit y every 8192 (truncated by up to 6e-5 of the sum of magnitudes), so that its truncation does
+ * not add up over K.  Any M >= 0, N, K >= 1, strides and element alignment; rows of x and w
  * that start on 16-byte boundaries are fastest.  Results repeat bit for bit.
  * DIT_ERR_INVALID_ARG: null pointers, negative sizes or strides, ldy < N, an unknown act, y at
  * residual's address with another stride.

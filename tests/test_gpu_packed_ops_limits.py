@@ -85,6 +85,22 @@ def test_linear_long_float32_sums_repeat_and_add_the_rest(m, n, k, dx):
         assert torch.equal(first, linear_fused(x, w, b, act="silu", residual=r, out_dtype=F32))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("m,n,k,dx", [(512, 512, 262144, 0), (500, 600, 131077, 1), (2048, 1024, 131072, 0), (1024, 4608, 70000, 0),
+                                      (512, 512, 8192, 0), (2048, 1024, 8200, 0), (1024, 4608, 16384, 0)])
+def test_linear_long_16_bit_sums(m, n, k, dx, dtype):
+    """The sum is taken over every 8192 products: 512 steps of at most 2^-22 of a sum that grows evenly, 513 / 2 2^-22 of the
+    whole, however long K is.  The rounding of an output is of either sign, at most u, 0.6 u in the root mean square: five
+    deviations of its mean over all outputs."""
+    x, w = same_signed(m, n, k, dtype, 0.25, dx, 0)
+    want = long_sum(x, w)
+    for _ in range(2):
+        off = (linear_fused(x, w).double() - want) / want
+        u = torch.finfo(dtype).eps / 2
+        assert off.mean().abs() <= 513 * 2.0 ** -23 + 5 * 0.6 * u / math.sqrt(m * n), off.mean().item()
+        assert off.abs().max() <= 513 * 2.0 ** -23 + u * (1 + 2.0 ** -10) + (k / 8192 + 8) * 2.0 ** -24, off.abs().max().item()
+
+
 # ------------------------------------------------------------------ attention
 
 
