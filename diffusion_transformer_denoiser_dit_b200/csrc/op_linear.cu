@@ -101,7 +101,9 @@ static cudaError_t launch_t(const LinearArgs& a, bool vec, int num_sms, cudaStre
   return launch_linear_tc(a, num_sms, st);
 }
 
-cudaError_t launch_linear_fused(const LinearArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_linear_fused(const LinearArgs& args, int num_sms, cudaStream_t st) {
+  LinearArgs a = args;
+  if (a.act == DIT_ACT_GELU && !a.out_f32) a.act = kActGelu16;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w)) & 15) == 0 &&
                    ((a.ldx | a.ldw) & 7) == 0;
   return a.fp16 ? launch_t<__half>(a, vec, num_sms, st) : launch_t<__nv_bfloat16>(a, vec, num_sms, st);

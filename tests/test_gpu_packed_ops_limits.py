@@ -101,6 +101,44 @@ def test_linear_long_16_bit_sums(m, n, k, dx, dtype):
         assert off.abs().max() <= 513 * 2.0 ** -23 + u * (1 + 2.0 ** -10) + (k / 8192 + 8) * 2.0 ** -24, off.abs().max().item()
 
 
+def activation(act, z, sixteen):
+    """Value in 64 bits and relative tolerance of the float32 one.  The sigmoid's exponent -z log2 e is rounded, by |z| 2^-24
+    of the result, as is its constant; two units of 2^-22 each and a few roundings: (|z| + 8) 2^-23.  Under the
+    tanh form its z is 2u, itself off by five roundings of 2^-24.  The erf form: 4.3e-7 of the polynomial, the
+    exponential and twice the reciprocal unit's 2^-22 and 2^-23, and six roundings make 1.3e-6 < 2^-19; for 16 bits 8.5e-6
+    of the polynomial and the exponent's rounding, at most 120 2^-24, besides: 1.7e-5 < 2^-15."""
+    if act == "gelu":
+        return z * torch.special.erfc(-z / math.sqrt(2.0)) / 2, torch.full_like(z, 2.0 ** -15 if sixteen else 2.0 ** -19)
+    w = z if act == "silu" else 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    return z * torch.sigmoid(w), ((1 if act == "silu" else 3.5) * w.abs() + 8) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("act,low", [("gelu", -12.5), ("silu", -80.0), ("gelu_tanh", -9.0)])
+@pytest.mark.parametrize("m", [1, 3, 200, 4096])
+def test_linear_activations_keep_their_tails(m, act, low):
+    """The argument is the bias alone, exact, from where the result leaves float32's range of digits up to 30."""
+    n = 4096
+    z = torch.cat([torch.linspace(low, 0, n // 2, device="cuda"), torch.linspace(0, 30, n // 2, device="cuda")])
+    for dtype in (BF16, FP16):
+        x, w = torch.zeros(m, 64, dtype=dtype, device="cuda"), torch.ones(n, 64, dtype=dtype, device="cuda")
+        want, tol = activation(act, z.double(), False)
+        got = linear_fused(x, w, z, act=act, out_dtype=F32).double()
+        assert ((got - want).abs() <= want.abs() * tol).all(), ((got - want) / want).abs().max().item()
+        want, tol = activation(act, z.double(), True)
+        got = linear_fused(x, w, z, act=act).double()
+        small = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps / 2   # half a step of the subnormal values
+        assert ((got - want).abs() <= want.abs() * (tol + torch.finfo(dtype).eps / 2 * (1 + 2.0 ** -10)) + small).all()
+
+
+def test_linear_activations_of_what_is_not_finite():
+    z = torch.tensor([NAN, INF, -INF, 1e30, -1e30, 0.0], device="cuda")
+    x, w = torch.zeros(2, 8, dtype=BF16, device="cuda"), torch.ones(6, 8, dtype=BF16, device="cuda")
+    for act in ("gelu", "silu", "gelu_tanh"):
+        for t in (F32, BF16):
+            y = linear_fused(x, w, z, act=act, out_dtype=t)[0]
+            assert torch.isnan(y[0]) and y[1] == INF and torch.isnan(y[2]) and y[3] == z[3].to(t) and y[4] == 0 and y[5] == 0
+
+
 # ------------------------------------------------------------------ attention
 
 
