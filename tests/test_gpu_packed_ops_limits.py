@@ -293,3 +293,21 @@ def test_attention_scores_that_overflow(form, sign):
     want, tol, lse_want, lse_tol = attention_want(q[:1], k[:kl[0]][keep], v[:kl[0]][keep], [1], [kl[0] - 1], False, 8.0)
     same(got[:1], want, tol, "out")
     same(lse[:, :1], lse_want, lse_tol, "lse")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("form", sorted(FORMS))
+def test_attention_one_key_with_nearly_all_weight(form, d):
+    """Scores of 10 at one key and small ones elsewhere: the log-sum-exp shows the error of that key's exponential alone, at
+    places that every unit computes.  Its tolerance (4.1e-5 at most by the count above) is far below 7e-5: an exponential
+    that is off by that at 2^0, as a cubic fitted on [-1/2, 1/2] is, does not pass."""
+    q, k, v, ql, kl = inputs(form, d, BF16, 21)
+    k = (k.float() * 0.05).to(BF16)
+    for at in (0, 3, 8, 9, 16):
+        one = k.clone()
+        one[at] = 0.25
+        qq = torch.full_like(q, 10 * d ** 0.5 / (0.25 * d))   # 10 = scale d 0.25 q
+        _, _, lse, tol = attention_want(qq, one, v, ql, kl, False, d ** -0.5)
+        assert tol[:, :ql[0]].max() < 5e-5
+        check_attention(qq, one, v, ql, kl, False)
+        check_attention(qq, one, v, ql, kl, True)
