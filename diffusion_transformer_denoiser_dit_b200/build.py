@@ -69,22 +69,36 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         list(ex.map(run, jobs))
     if jobs or _needs(LIB, objs):
         run([nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", LIB] + objs + ["-lcudart_static", "-ldl", "-lrt", "-lpthread"])
-    build_fastcall(run)
+    build_fastcall(verbose or ptxas_verbose)
     return LIB
 
 
-def build_fastcall(run):
+def build_fastcall(verbose: bool = False):
+    """Optional: what cannot be built here is left out with a warning, and an older one does not stay."""
     spec, python = importlib.util.find_spec("torch"), sysconfig.get_paths()["include"]
-    if spec is None or shutil.which("g++") is None or not os.path.exists(os.path.join(python, "Python.h")):
-        return
-    torch = os.path.dirname(spec.origin)
-    inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
     src = os.path.join(CSRC, "fastcall.cpp")
-    if _needs(FASTCALL, [src, os.path.join(INCLUDE, "dit.h"), os.path.join(torch, "version.py")]):
-        cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
-        run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE, "-I", python, "-isystem", inc, "-isystem",
-             os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, src, "-o", FASTCALL, "-L", lib,
-             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    deps = [src, os.path.join(INCLUDE, "dit.h")]
+    torch = os.path.dirname(spec.origin) if spec is not None else None
+    if torch:
+        deps.append(os.path.join(torch, "version.py"))
+    if not _needs(FASTCALL, deps):
+        return
+    if os.path.exists(FASTCALL):
+        os.remove(FASTCALL)
+    if torch is None or shutil.which("g++") is None or not os.path.exists(os.path.join(python, "Python.h")):
+        return
+    inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE, "-I", python, "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, src, "-o", FASTCALL, "-L", lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose:
+        sys.stdout.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        if os.path.exists(FASTCALL):
+            os.remove(FASTCALL)
+        sys.stderr.write(r.stderr + "warning: _fastcall.so was not built (calls go through ctypes): " + " ".join(cmd) + "\n")
 
 
 if __name__ == "__main__":
