@@ -373,6 +373,13 @@ def _no_dtype(name: str, dtype):
     raise TypeError(f"{name}: dtype {dtype} is not supported")
 
 
+def _status(rt: _Runtime, name: str, status):
+    """Address of the int32 that a wait which ran out writes."""
+    if status.dtype != rt.int32 or status.numel() < 1:
+        raise ValueError(f"{name}: status int32 [1]")
+    return status.data_ptr()
+
+
 def _elsewhere(rt: _Runtime, name: str, fn, dev: int, tensors, stream, args):
     """fn(*args, stream) off the common path: refuses what is not on one CUDA device, takes a given
     stream, or enters the tensors' device when another is current."""
@@ -462,7 +469,7 @@ def linear_fused(x, w, bias=None, act: str = "none", residual=None, out=None, ou
             raise ValueError("linear_fused: residual [M, N] of out's dtype")
         pr, ldr, same = residual.data_ptr(), residual.stride(0), same and residual.get_device() == dev
     if status is not None:
-        ps, same = status.data_ptr(), same and status.get_device() == dev
+        ps, same = _status(rt, name, status), same and status.get_device() == dev
     if out is None:
         out = _fresh(x, (M, N), odtype, stream)
     args = (code, x.data_ptr(), ldx, w.data_ptr(), ldw, pb, a, pr, ldr, out.data_ptr(), ldy, ocode, M, N, K, ps)
@@ -522,7 +529,7 @@ def attention_packed(q, k, v, cu_q, cu_k, max_q: int, max_k: int, causal: bool =
     lse = _fresh(q, (h, tq), rt.float32, stream) if return_lse else None
     args = (code, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
             cu_q.data_ptr(), cu_k.data_ptr(), n, tq, tk, max_q, max_k, h, hk, d, strides,
-            d ** -0.5 if scale is None else scale, 1 if causal else 0, None if status is None else status.data_ptr())
+            d ** -0.5 if scale is None else scale, 1 if causal else 0, None if status is None else _status(rt, name, status))
     if same and stream is None and dev >= 0 and dev == rt.current_device():
         rc = rt.attention(*args, rt.raw_stream(dev))
     else:
