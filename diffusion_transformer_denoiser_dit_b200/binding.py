@@ -508,12 +508,12 @@ def attention_packed(q, k, v, cu_q, cu_k, max_q: int, max_k: int, causal: bool =
             return y if type(y) is not int else _refused(name, y)
     _need(q.dim() == 3 and k.dim() == 3 and k.shape == v.shape, "attention_packed: q [total_q, heads, dh], k and v "
           "[total_k, kv_heads, dh]")
-    (tq, h, d), (tk, hk, dk), dtype, n = q.shape, k.shape, q.dtype, cu_q.shape[0] - 1
+    (tq, h, d), (tk, hk, dk), dtype, n = q.shape, k.shape, q.dtype, cu_q.numel() - 1
     code = rt.code16.get(dtype)
     if code is None:
         _no_dtype(name, dtype)
-    if d != dk or k.dtype != dtype or v.dtype != dtype:
-        raise ValueError("attention_packed: q, k and v of one dtype and feature count")
+    if d != dk or d < 1 or k.dtype != dtype or v.dtype != dtype:
+        raise ValueError("attention_packed: q, k and v of one dtype and number of features, at least 8")
     if (cu_q.dim() != 1 or n < 0 or cu_k.shape != cu_q.shape or cu_q.dtype != rt.int32 or cu_k.dtype != rt.int32
             or not cu_q.is_contiguous() or not cu_k.is_contiguous()):
         raise ValueError("attention_packed: cu_q and cu_k contiguous int32 [n + 1]")
