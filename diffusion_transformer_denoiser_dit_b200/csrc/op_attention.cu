@@ -26,6 +26,7 @@
 // Every wait is bounded; no TMA multicast.
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -897,10 +898,10 @@ template <int NA, typename T, bool SPLIT>
 static cudaError_t set_up_fa(int (&places)[4]) {
   using C = FaCfg<NA, SPLIT>;
   auto kernel = attention_tc_kernel<NA, T, SPLIT>;
-  static int of[kMaxDevices][4] = {};
+  static std::atomic<int> of[kMaxDevices][4];  // published together, the first last: threads may come at once
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
-  if (of[dev][0] == 0) {
+  if (of[dev][0].load(std::memory_order_acquire) == 0) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     // the register split (setmaxnreg) must fit in the launch allocation, or it would wait forever
@@ -922,10 +923,12 @@ static cudaError_t set_up_fa(int (&places)[4]) {
       e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
       if (e != cudaSuccess) return e;
       if (n <= 0) return cudaErrorInvalidConfiguration;
-      of[dev][i] = n;
+      places[i] = n;
     }
+    for (int i = 3; i >= 0; --i) of[dev][i].store(places[i], std::memory_order_release);
+    return cudaSuccess;
   }
-  for (int i = 0; i < 4; ++i) places[i] = of[dev][i];
+  for (int i = 0; i < 4; ++i) places[i] = of[dev][i].load(std::memory_order_relaxed);
   return cudaSuccess;
 }
 

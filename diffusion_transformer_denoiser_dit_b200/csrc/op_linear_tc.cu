@@ -23,6 +23,7 @@
 // that grows evenly (measured 3.5e-5 with bfloat16 products, 5.3e-5 with fp16 ones), an eighth of fp16's half step.
 //
 // Every wait is bounded; no TMA multicast.
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -920,13 +921,14 @@ static cudaError_t launch_split(const LinearArgs& a, const CUtensorMap& tx, cons
   return cudaLaunchKernelEx(&cfg, kernel, tx, tw, a, sp, box_rows);
 }
 
-// clusters of 1, 2, 4 and 8 CTAs of the split kernel that the device runs at one time
+// clusters of 1, 2, 4 and 8 CTAs of the split kernel that the device runs at one time; first calls may come
+// from several threads at once, so the counts are published together, the last with release
 template <typename T>
 static bool split_clusters(int* fit) {
-  static int of[kMaxDevices][4] = {};
+  static std::atomic<int> of[kMaxDevices][4];
   const int dev = current_device();
   if (dev < 0) return false;
-  if (of[dev][3] == 0) {
+  if (of[dev][3].load(std::memory_order_acquire) == 0) {
     auto kernel = linear_split_kernel<64, T, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SplitCfg<64>::SMEM) != cudaSuccess) return false;
     for (int i = 0; i < 4; ++i) {
@@ -939,13 +941,12 @@ static bool split_clusters(int* fit) {
       at[0].val.clusterDim = {1u << i, 1, 1};
       cfg.attrs = at;
       cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&of[dev][i], kernel, &cfg) != cudaSuccess || of[dev][i] <= 0) {
-        of[dev][3] = 0;
-        return false;
-      }
+      if (cudaOccupancyMaxActiveClusters(&fit[i], kernel, &cfg) != cudaSuccess || fit[i] <= 0) return false;
     }
+    for (int i = 0; i < 4; ++i) of[dev][i].store(fit[i], std::memory_order_release);
+    return true;
   }
-  for (int i = 0; i < 4; ++i) fit[i] = of[dev][i];
+  for (int i = 0; i < 4; ++i) fit[i] = of[dev][i].load(std::memory_order_relaxed);
   return true;
 }
 
