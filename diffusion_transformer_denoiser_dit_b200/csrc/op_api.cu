@@ -200,8 +200,7 @@ dit_status dit_op_rotary(const dit_rotary* r, int dtype, const void* x, long lon
       !distinct(tokens, y_tok, heads, y_head, dh) || (x == y && (x_tok != y_tok || x_head != y_head)))
     return DIT_ERR_INVALID_ARG;
   if (static_cast<long long>(heads) * dh > (1 << 24) || tokens > kMaxSize) return DIT_ERR_UNSUPPORTED;
-  const int sms = current_sms();
-  if (sms == 0) return DIT_ERR_NO_DEVICE;
+  if (current_sms() == 0) return DIT_ERR_NO_DEVICE;
   RotaryArgs a;
   a.x = x;
   a.pos = positions;
@@ -217,7 +216,7 @@ dit_status dit_op_rotary(const dit_rotary* r, int dtype, const void* x, long lon
   a.pos64 = positions_64bit != 0;
   a.interleaved = interleaved != 0;
   a.transpose = transpose != 0;
-  return launched(launch_rotary(*r, a, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(launch_rotary(*r, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

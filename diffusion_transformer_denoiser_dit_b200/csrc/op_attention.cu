@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(640, 1)
     if (lane == 0) mbar_arrive(bar(B::IE + (n & 1)));
     return ok && it.ntok >= 0;
   };
-  // a wait that ran out: the role does no more work, but keeps step in the exchanges
-  // split form, many rows: they are exchanged through the K / V slots once every CTA is done with them
+  // Split form, many rows: they are exchanged through the K / V slots once every CTA is done with them.  A role
+  // whose wait ran out does no more work, but keeps step here.
   auto exchange_others = [&]() {
     if (SPLIT && !f.light) {
       __syncwarp();

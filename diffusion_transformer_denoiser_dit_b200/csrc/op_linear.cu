@@ -53,6 +53,8 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const LinearArgs a, co
     }
     k = kv;
   }
+  // what is left of K; all of it where rows are not 16-byte aligned (M = 1), two bytes per load: 1151 -> 4608 9.3 us for
+  // 3.8, 8191 -> 8192 81 for 22.7
   for (int kk = k + slice * 32 + lane; kk < a.K; kk += ks * 32) {
 #pragma unroll
     for (int i = 0; i < NR; ++i) {

@@ -962,7 +962,10 @@ static cudaError_t launch_tc(const LinearArgs& a, int num_sms, cudaStream_t st) 
   auto rounds = [&](int bn) { return (mt2 * ((a.N + bn - 1) / bn) + pairs - 1) / pairs; };
   const int bn2 = rounds(192) * 400 < rounds(256) * 512 ? 192 : 256;
   // fewer tiles than half the pairs: the split kernel (1024 x 1152 -> 4608, 72 of 74 pairs busy: 12.9
-  // against 24.6 us; 512 x 768 -> 2304, 24 busy: 8.5 against 8.0)
+  // against 24.6 us; 512 x 768 -> 2304, 24 busy: 8.5 against 8.0).  Tiles of 256 rows are counted, full or not: up to
+  // 128 rows by 7200 features and more the split kernel would mostly last less (in a graph, 5 x 4608 -> 7200 12.6 against
+  // 30.8 us, 128 x 1152 -> 16384 10.0 against 11.9; 64 x 1152 -> 32768 17.6 against 16.7), above 128 not
+  // (192 x 1152 -> 16384 18.9 against 12.0).
   if (mt2 * ((a.N + 191) / 192) >= pairs / 2 && map_rows(&tx, dt, a.x, a.M, a.K, a.ldx, 128, 64) &&
       map_rows(&tw, dt, a.w, a.N, a.K, a.ldw, bn2 / 2, 64)) {
     if (a.out_f32) return bn2 == 192 ? launch_pair<192, T, true>(a, tx, tw, num_sms, st) : launch_pair<256, T, true>(a, tx, tw, num_sms, st);

@@ -44,8 +44,9 @@ __global__ void __launch_bounds__(kRotaryThreads, 10)
   __syncthreads();
   // A thread keeps its pairs c of a row (one head of one token) and steps through the rows of the block's
   // tokens; it also copies every pc-th vector behind the turned part.  One row at a time in small blocks:
-  // ten blocks of an SM overlap their loads (32768 x 20 x 128 bf16, half turned: 55 us, 6.1 TB/s; all
-  // turned: 61 us, with four rows in flight per thread and three blocks of 256: 123 us).
+  // ten blocks of an SM overlap their loads (32768 x 20 x 128 bf16, half turned: 54 us, 6.2 TB/s; all
+  // turned: 61 us, with four rows in flight per thread and three blocks of 256: 123 us).  The bound of ten leaves 48
+  // registers, which the 16-bit kernels of eight elements exceed by 8 to 16 spilled bytes; with nine blocks, and none: 59 us.
   const int pc = P / V;
   for (int c0 = 0; c0 < pc; c0 += kRotaryThreads) {
     const int wide = min(pc - c0, kRotaryThreads), together = kRotaryThreads / wide;  // rows at a time
@@ -109,7 +110,7 @@ static cudaError_t launch_t(const dit_rotary& r, const RotaryArgs& a, cudaStream
   return launch_v<T, 1>(r, a, st);
 }
 
-cudaError_t launch_rotary(const dit_rotary& r, const RotaryArgs& a, int, cudaStream_t st) {
+cudaError_t launch_rotary(const dit_rotary& r, const RotaryArgs& a, cudaStream_t st) {
   if (a.dtype == DIT_DTYPE_BF16) return launch_t<__nv_bfloat16>(r, a, st);
   if (a.dtype == DIT_DTYPE_FP16) return launch_t<__half>(r, a, st);
   return launch_t<float>(r, a, st);

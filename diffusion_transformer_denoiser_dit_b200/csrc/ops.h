@@ -52,7 +52,7 @@ struct RotaryArgs {
   int tokens, heads, dh;
   int dtype, pos64, interleaved, transpose;
 };
-cudaError_t launch_rotary(const dit_rotary& r, const RotaryArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_rotary(const dit_rotary& r, const RotaryArgs& a, cudaStream_t st);
 
 // Tensor map of a strided view: dims[0] contiguous, strides_bytes[i] from dims[i] to dims[i+1],
 // box[0] 128 bytes wide, 128-byte swizzle.  False where TMA cannot read it.

@@ -399,7 +399,9 @@ int dit_forward_launch_count(const dit_handle* h, int B, float cfg_scale);
 /* DIT_DTYPE_FP16 (16-bit patterns); strides are in elements.  No block allocates,  */
 /* keeps anything between calls or synchronises, so any number may be in flight on  */
 /* any streams and in captured graphs.  status: dev int32 or NULL; it receives      */
-/* DIT_ERR_DEVICE_TIMEOUT if a bounded wait in the kernel runs out (0 stays 0).     */
+/* DIT_ERR_DEVICE_TIMEOUT if a bounded wait in the kernel runs out (0 stays 0); with */
+/* NULL nothing tells of that.  Sums of products are the tensor cores' float32, which */
+/* cuts a product, or a sum, below about 2^-23 of the sum so far.                     */
 /* ------------------------------------------------------------------------------ */
 
 enum { DIT_ACT_NONE = 0, DIT_ACT_RELU = 1, DIT_ACT_GELU_TANH = 2, DIT_ACT_GELU = 3, DIT_ACT_SILU = 4 };
@@ -441,7 +443,8 @@ dit_status dit_op_linear_fused(int dtype, const void* x, long long ldx, const vo
  * rows outside are not used.  Offsets beyond the totals are cut to them.  max_q, max_k: the
  * longest query and key length, which only choose how the work is split.
  * nq = 1 is the form for single new tokens over a cache.  The scores stay float32; the
- * probabilities are rounded to dtype for the product with v, their sum is not.  v's rows
+ * probabilities are rounded to dtype for the product with v, their sum is not; that product is
+ * cut as above, by up to 6e-5 of its value per 8192 keys that one CTA takes.  v's rows
  * within a sequence have to be finite (a masked probability is 0, and 0 * inf is NaN).
  * Results repeat bit for bit.  DIT_ERR_UNSUPPORTED: another dtype, dh not a multiple of 8 or
  * above 128, more than 128 heads per key head, (total_q + n_seq) * kv_heads above 2^31 - 65537.
