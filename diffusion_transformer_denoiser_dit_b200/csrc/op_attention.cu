@@ -8,7 +8,9 @@
 //   read from there.  Two threads per row: with one, the two warps of a scheduler left it idle half
 //   the time (period of a tile pair at dh = 64: 3100 cycles for 1536 of exponentials).
 // O is rescaled only when the maximum grew by more than 2^8 (then in place, by its own threads),
-// so P <= 2^8 before the final division.  V is used as it lies (keys x features: the MN-major B
+// so P <= 2^8 before the final division.  P is rounded to the type of V, since the MMA takes both operands in one
+// 16-bit type: one rounding per key, averaged over the keys, beside that of the output (against 64 bits, 8192 tokens bfloat16,
+// 2.0e-3 of the norm for 1.5e-3 with P in float32).  Its sum l, by which O is divided, is not rounded.  V is used as it lies (keys x features: the MN-major B
 // operand of the MMA).
 //
 // Pair form: an item is two neighbouring query tiles of one key head; both read the same K / V

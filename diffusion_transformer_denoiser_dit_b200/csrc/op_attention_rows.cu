@@ -15,6 +15,8 @@
 // 160 -> 70 us; 256 x 1024 keys, 8 key heads of 128, 195 -> 185 us (5.8 TB/s).  The step is a chain (loads,
 // Q K^T, maximum, exponentials, P V), so few long sequences stay with the other kernel.  Tried: K and V staged
 // in shared memory three steps ahead, slower (211 us; 20 x 300 keys 11.8 against 9.0: fewer CTAs per SM).
+// P is rounded to the type of V, as the products' operands need it; its sum is not.  That is a rounding per key beside that of
+// the output: against 64 bits, 256 x 1024 keys of 128, 2.3e-3 of the norm in bfloat16 for 1.7e-3 with P in float32.
 // Partial rows are joined in a fixed order: warps in shared memory, CTAs over distributed shared memory.
 #include <math.h>
 
